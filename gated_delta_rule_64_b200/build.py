@@ -3,7 +3,7 @@
     python -m gated_delta_rule_64_b200.build [--force] [--verbose] [--checked]
 
 Every ``csrc/*.cu`` file is compiled for sm_100a only and linked into
-``gated_delta_rule_64_b200/libgdn.so``; the header is ``include/gdn.h``.
+``gated_delta_rule_64_b200/libgdn.so``; the headers are ``include/*.h``.
 ``--checked`` builds ``libgdn_checked.so`` instead, with -DGDN_CHECKED: the
 chunked-prefill kernels then check the ranges they derive from the sizes they
 are given and report a failed check in the call's status word (for tests; the
@@ -42,7 +42,8 @@ def sources() -> list[str]:
 
 
 def deps() -> list[str]:
-    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "gdn.h")]
+    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
+        glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date(lib: str = LIB) -> bool:

@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "api_checks.cuh"
 #include "gdn_internal.cuh"
 
 namespace gdn {
@@ -95,8 +96,6 @@ LaunchScope::~LaunchScope() {
 // ---------------------------------------------------------------------------
 // Workspace plan of the chunked forward pass
 // ---------------------------------------------------------------------------
-static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 ChunkPlan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
     ChunkPlan p{};
     p.N = num_seqs;
@@ -155,12 +154,11 @@ ChunkPlan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
 }
 
 // ---------------------------------------------------------------------------
-// Validation helpers
+// Validation helpers (the pointer and range checks are in api_checks.cuh)
 // ---------------------------------------------------------------------------
-static bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-static bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+void clear_error() { g_last_error[0] = 0; }
 
-static gdn_status check_desc(const gdn_desc *d) {
+gdn_status check_desc(const gdn_desc *d) {
     if (!d) return fail(GDN_ERR_INVALID_ARG, "descriptor is NULL");
     if (d->B < 0 || d->T < 0 || d->H <= 0)
         return fail(GDN_ERR_INVALID_ARG, "need B >= 0, T >= 0, H > 0 (got B=%lld T=%lld H=%lld)",
@@ -183,12 +181,6 @@ static gdn_status check_desc(const gdn_desc *d) {
     if (elems > 4.0e15) return fail(GDN_ERR_INVALID_ARG, "problem too large");
     return GDN_OK;
 }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-static bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-static Range range_of(const void *p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + bytes}; }
 
 }  // namespace gdn
 

@@ -1,0 +1,125 @@
+// Linear attention with a decay for each head: what its kernels share.
+//
+//     S_t = alpha_t S_{t-1} + v_t k_t^T,   o_t = S_t (scale q_t)
+//
+// Chunkwise form.  For a chunk of L tokens with start state S0, G_i = sum_{j <= i} g_j
+// (log2 units throughout the kernels) and G = G_L:
+//     o_i = scale 2^{G_i} S0 q_i + sum_{j <= i} scale 2^{G_i - G_j} (q_i . k_j) v_j
+//     S   = 2^G S0 + sum_j 2^{G - G_j} v_j k_j^T
+// Every exponent is <= 0.  Nothing but the d_v x d_k state passes from chunk to chunk,
+// and its update is a plain sum: a segment of chunks contributes
+// U = sum_j 2^{(decay from j to the segment's end)} v_j k_j^T whatever state it starts
+// from.  So a long sequence is cut into segments of `seg` tokens: the state kernel
+// forms every segment's U (all segments but each sequence's last, from its end
+// backwards until nothing reaches the end any more), the combine kernel chains the start states
+// S_{g+1} = 2^{G_g} S_g + U_g, and the output kernel runs all segments side by side.
+// Sequences of one segment need the output kernel alone.
+#pragma once
+
+#include "chunk_common.cuh"
+#include "gdn_internal.cuh"
+#include "gdn_linattn.h"
+
+namespace gdn {
+namespace lin {
+
+constexpr float kLog2e = 1.4426950408889634f;
+// A decay below 2^-150 gives exactly zero in fp32 (the kernels flush from 2^-126 on).
+constexpr float kDead = -150.f;
+
+struct Plan {
+    int64_t N, rows, T, H, Hk, dk, dv;
+    bool packed, tc, fixed_gate;
+    int64_t seg;     // tokens per segment, a multiple of 64
+    int64_t G;       // fixed-length sequences: segments per sequence (>= 1)
+    int64_t slots;   // segments in all (packed: an upper bound)
+    int64_t sslots;  // segments of sequences that have more than one (packed: an upper bound; 0: none has)
+    size_t off_status, off_tot, off_state, total;
+};
+Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed);
+
+struct Args {
+    const void *q, *k, *v;
+    const float *g, *h0;
+    const int32_t *cu;
+    int64_t T, N, rows, H, Hk, seg, G, slots, sslots;
+    float scale;
+    int64_t snap_stride, n_snap;
+    void *out;
+    float *final_state, *snaps;
+    double *tot;     // [sslots][H] decay of a segment, log2 units
+    float *states;   // [sslots][H][d_v][d_k]: U of a segment, then its start state
+    int *status;
+};
+
+// A segment: the j-th of the nseg of sequence n, token rows [start, start + len), `pos`
+// tokens into the sequence; ss is its place in the workspace (nseg > 1 only).
+//
+// Two numberings find it.  `slots` counts every segment (the output kernel's blocks):
+// packed sequence n owns the slots from cu[n] / seg + n on.  They are enough, since
+// floor(b/s) - floor(a/s) + 1 >= ceil((b - a)/s), and an empty sequence has one.  `sslots`
+// counts the segments of sequences longer than one segment only (the state kernel's
+// blocks and the workspace): from floor(2 cu[n] / seg) on, enough since
+// floor(2 len / seg) >= ceil(len / seg) for len > seg.
+struct Slot {
+    int64_t n, j, nseg, start, pos, len, ss;
+};
+__device__ __forceinline__ int64_t clamped_cu(const Args &a, int64_t n) {
+    const int64_t c = a.cu[n];
+    return c < 0 ? 0 : (c > a.rows ? a.rows : c);
+}
+__device__ __forceinline__ int64_t state_base(const Args &a, int64_t n) {
+    return a.cu ? 2 * clamped_cu(a, n) / a.seg : n * a.G;
+}
+template <bool STATE>
+__device__ __forceinline__ bool locate(const Args &a, int64_t slot, Slot &s) {
+    int64_t base;
+    if (a.cu) {
+        auto base_of = [&](int64_t n) { return STATE ? state_base(a, n) : clamped_cu(a, n) / a.seg + n; };
+        int64_t lo = 0, hi = a.N;  // the last sequence whose first slot is not past `slot`
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) / 2;
+            if (base_of(mid) <= slot) lo = mid; else hi = mid;
+        }
+        s.n = lo;
+        base = base_of(lo);
+    } else {
+        s.n = slot / a.G;
+        base = s.n * a.G;
+    }
+    s.j = slot - base;
+    if (s.n >= a.N || s.j < 0) return false;
+    int64_t start, len;
+    seq_bounds(a.cu, s.n, a.T, a.rows, start, len);
+    s.nseg = len > 0 ? (len + a.seg - 1) / a.seg : 1;
+    if (s.j >= s.nseg) return false;
+    s.pos = s.j * a.seg;
+    s.start = start + s.pos;
+    s.len = len - s.pos < a.seg ? len - s.pos : a.seg;
+    s.ss = state_base(a, s.n) + s.j;
+    return s.nseg == 1 || s.ss < a.sslots;  // (wrong offsets stay inside the workspace)
+}
+
+// 2^x for a decay x <= 0 in 64 bits as two floats: a fixed decay close to 1, applied
+// once a chunk over a very long sequence, must not carry the same rounding every time.
+__device__ __forceinline__ float2 exp2_pair(double x) {
+    const double e = exp2(x);
+    const float hi = (float)e;
+    return make_float2(hi, (float)(e - (double)hi));
+}
+
+gdn_status launch_simt(const Plan &p, const Args &a, int dtype, cudaStream_t s);
+gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s);
+gdn_status launch_combine(const Plan &p, const Args &a, cudaStream_t s);
+gdn_status launch_decode(const gdn_desc &d, const void *q, const void *k, const void *v, const float *g, float *state,
+                         void *out, cudaStream_t s);
+gdn_status launch_qk_norm_rope(const gdn_qk_rope_desc &d, const void *q, const void *k, const int32_t *pos,
+                               const float *inv_freq, const float *qw, const float *kw, void *q_out, void *k_out,
+                               cudaStream_t s);
+size_t beam_workspace(const gdn_beam_desc &d);
+gdn_status launch_beam_select(const gdn_beam_desc &d, const void *logits, const float *scores, float *out_scores,
+                              int32_t *out_parent, int32_t *out_token, void *ws, cudaStream_t s);
+gdn_status launch_state_reorder(void *state, const int32_t *parent, int64_t B, int W, size_t row_bytes, cudaStream_t s);
+
+}  // namespace lin
+}  // namespace gdn

@@ -1,0 +1,364 @@
+// Chunkwise linear attention with a decay for each head, on the CUDA cores: fp32
+// inputs, and bf16 inputs of head widths the tensor-core path does not take.  Also the
+// combine kernel, which both paths share.  The algebra is at the top of linattn.cuh.
+//
+// One block works on 32 state rows (value channels) of one segment and head, which
+// stay in shared memory in fp32 for the whole segment, in chunks of 32 tokens: the
+// scores Q K^T (32 x 32) of a chunk are formed by each of the d_v / 32 blocks that share
+// a head, a third of the multiply-adds at d_k = 128, in exchange for four times
+// as many blocks.  All sums are fp32.  The decays into and out of a chunk are sums of just
+// the gates they cover; those between two tokens of a chunk are differences of prefix
+// sums, held in 64 bits, since a gate that erases the state (-1e4, say) would leave
+// nothing of its neighbours in fp32.
+#include "linattn.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace lin {
+namespace {
+
+using sm100::ex2;
+
+constexpr int kC = 32;        // tokens per chunk
+constexpr int kRows = 32;     // state rows per block
+constexpr int kThreads = 256;
+
+// Gate g of token row `row` and head h, in log2 units.
+__device__ __forceinline__ float gate2(const Args &a, bool fixed, int64_t row, int64_t h) {
+    return a.g[fixed ? h : row * a.H + h] * kLog2e;
+}
+
+// Inclusive prefix sum over the warp, and the sum of what follows the lane.
+template <typename Sum>
+__device__ __forceinline__ void warp_scans(float x, int lane, Sum &prefix, float &after) {
+    prefix = x;
+    after = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum p = __shfl_up_sync(0xffffffffu, prefix, o);
+        const float s = __shfl_down_sync(0xffffffffu, after, o);
+        if (lane >= o) prefix += p;
+        if (lane + o < 32) after += s;
+    }
+    const float s = __shfl_down_sync(0xffffffffu, after, 1);
+    after = lane < 31 ? s : 0.f;
+}
+
+__device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float c) {
+    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+}
+
+// Four consecutive values as fp32 (16-byte aligned fp32, 8-byte aligned bf16).
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+}
+
+// `n` rows of W values (rows >= len: zeros, not read), `ld` elements apart, into shared rows of LD floats.
+template <int W, int LD, typename Tin>
+__device__ __forceinline__ void stage_rows(float *dst, const Tin *src, int64_t ld, int len) {
+    for (int e = threadIdx.x; e < kC * (W / 4); e += kThreads) {
+        const int r = e / (W / 4), c = e % (W / 4) * 4;
+        const float4 x = r < len ? load4(src + r * ld + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(dst + r * LD + c) = x;
+    }
+}
+
+template <int DK>
+struct Smem {
+    static constexpr int LK = DK + 4, LV = kRows + 4, LP = kC + 1;  // padded rows: no bank conflicts
+    float q[kC * LK], k[kC * LK], S[kRows * LK], v[kC * LV], P[kC * LP];
+    double G[kC];               // per token: prefix sum of the gates
+    float w[kC], e[kC];         // decay to the chunk's end; scale * decay from its start
+    float2 decay;               // of the whole chunk
+};
+
+// Outputs of one segment, head and 32 value channels, from the segment's start state.
+template <int DK, typename Tin>
+__global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64_t dv, bool fixed) {
+    extern __shared__ float4 smem_raw[];
+    using Sm = Smem<DK>;
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
+    constexpr int LK = Sm::LK, LV = Sm::LV, LP = Sm::LP;
+    constexpr int TR = DK / 32;  // state rows of a thread, four columns each
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slices = (int)(dv / kRows);
+    const int64_t id = blockIdx.x;
+    const int64_t h = id / slices % a.H;
+    const int r0 = (int)(id % slices) * kRows;
+    Slot s;
+    if (!locate<false>(a, id / slices / a.H, s)) return;
+    const int64_t hq = h / (a.H / a.Hk);
+    const Tin *q = static_cast<const Tin *>(a.q) + (s.start * a.Hk + hq) * DK;
+    const Tin *k = static_cast<const Tin *>(a.k) + (s.start * a.Hk + hq) * DK;
+    const Tin *v = static_cast<const Tin *>(a.v) + (s.start * a.H + h) * dv + r0;
+    Tin *out = static_cast<Tin *>(a.out) + (s.start * a.H + h) * dv + r0;
+    const int64_t ldk = a.Hk * DK, ldv = a.H * dv;
+    // this thread's part of the state: rows sr .. sr + TR - 1, columns sc .. sc + 3
+    const int sc = tid % (DK / 4) * 4, sr = tid / (DK / 4) * TR;
+    const float *from = s.nseg > 1 ? a.states + (s.ss * a.H + h) * dv * DK
+                                   : (a.h0 ? a.h0 + (s.n * a.H + h) * dv * DK : nullptr);
+#pragma unroll
+    for (int i = 0; i < TR; ++i)
+        *reinterpret_cast<float4 *>(sm.S + (sr + i) * LK + sc) =
+            from ? load4(from + (int64_t)(r0 + sr + i) * DK + sc) : make_float4(0.f, 0.f, 0.f, 0.f);
+
+    for (int64_t t0 = 0; t0 < s.len; t0 += kC) {
+        const int L = (int)(s.len - t0 < kC ? s.len - t0 : kC);
+        __syncthreads();  // the previous chunk is done with the tiles
+        stage_rows<DK, LK>(sm.q, q + t0 * ldk, ldk, L);
+        stage_rows<DK, LK>(sm.k, k + t0 * ldk, ldk, L);
+        stage_rows<kRows, LV>(sm.v, v + t0 * ldv, ldv, L);
+        if (warp == 0) {
+            const float g = lane < L ? gate2(a, fixed, s.start + t0 + lane, h) : 0.f;
+            double G;
+            float after;
+            warp_scans(g, lane, G, after);
+            sm.G[lane] = G;
+            sm.w[lane] = ex2(after);
+            sm.e[lane] = a.scale * ex2((float)G);
+            // the chunk's decay: a fixed gate's product in 64 bits, a token gate's sum
+            if (lane == 31) sm.decay = exp2_pair(fixed ? (double)a.g[h] * 1.4426950408889634074 * L : G);
+        }
+        __syncthreads();
+        // scores: this thread's tokens i = ti, ti + 16 against j = tj, tj + 16
+        const int tj = lane & 15, ti = warp * 2 + (lane >> 4);
+        {
+            float acc[2][2] = {};
+#pragma unroll 8
+            for (int c = 0; c < DK; c += 4) {
+                const float4 q0 = *reinterpret_cast<const float4 *>(sm.q + ti * LK + c);
+                const float4 q1 = *reinterpret_cast<const float4 *>(sm.q + (ti + 16) * LK + c);
+                const float4 k0 = *reinterpret_cast<const float4 *>(sm.k + tj * LK + c);
+                const float4 k1 = *reinterpret_cast<const float4 *>(sm.k + (tj + 16) * LK + c);
+                acc[0][0] = dot4(q0, k0, acc[0][0]);
+                acc[0][1] = dot4(q0, k1, acc[0][1]);
+                acc[1][0] = dot4(q1, k0, acc[1][0]);
+                acc[1][1] = dot4(q1, k1, acc[1][1]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int i = ti + 16 * x, j = tj + 16 * y;
+                    sm.P[i * LP + j] = j <= i ? a.scale * ex2((float)(sm.G[i] - sm.G[j])) * acc[x][y] : 0.f;
+                }
+        }
+        __syncthreads();
+        // outputs: tokens ti, ti + 16, channels tj, tj + 16
+        {
+            float acc[2][2] = {};
+#pragma unroll 8
+            for (int c = 0; c < DK; c += 4) {
+                const float4 q0 = *reinterpret_cast<const float4 *>(sm.q + ti * LK + c);
+                const float4 q1 = *reinterpret_cast<const float4 *>(sm.q + (ti + 16) * LK + c);
+                const float4 s0 = *reinterpret_cast<const float4 *>(sm.S + tj * LK + c);
+                const float4 s1 = *reinterpret_cast<const float4 *>(sm.S + (tj + 16) * LK + c);
+                acc[0][0] = dot4(q0, s0, acc[0][0]);
+                acc[0][1] = dot4(q0, s1, acc[0][1]);
+                acc[1][0] = dot4(q1, s0, acc[1][0]);
+                acc[1][1] = dot4(q1, s1, acc[1][1]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) acc[x][y] *= sm.e[ti + 16 * x];
+            for (int j = 0; j < L; ++j) {
+                const float v0 = sm.v[j * LV + tj], v1 = sm.v[j * LV + tj + 16];
+                const float p0 = sm.P[ti * LP + j], p1 = sm.P[(ti + 16) * LP + j];
+                acc[0][0] = fmaf(p0, v0, acc[0][0]);
+                acc[0][1] = fmaf(p0, v1, acc[0][1]);
+                acc[1][0] = fmaf(p1, v0, acc[1][0]);
+                acc[1][1] = fmaf(p1, v1, acc[1][1]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    if (ti + 16 * x < L) out[(t0 + ti + 16 * x) * ldv + tj + 16 * y] = from_f32<Tin>(acc[x][y]);
+        }
+        __syncthreads();
+        // S = 2^G S + sum_j w_j v_j k_j^T
+        {
+            float acc[TR][4] = {};
+            for (int j = 0; j < L; ++j) {
+                const float4 kk = *reinterpret_cast<const float4 *>(sm.k + j * LK + sc);
+                const float w = sm.w[j];
+#pragma unroll
+                for (int i = 0; i < TR; ++i) {
+                    const float x = w * sm.v[j * LV + sr + i];
+                    acc[i][0] = fmaf(x, kk.x, acc[i][0]);
+                    acc[i][1] = fmaf(x, kk.y, acc[i][1]);
+                    acc[i][2] = fmaf(x, kk.z, acc[i][2]);
+                    acc[i][3] = fmaf(x, kk.w, acc[i][3]);
+                }
+            }
+            const float2 d = sm.decay;
+            const int64_t done = s.pos + t0 + L;  // tokens of the sequence so far
+            const bool snap = a.n_snap > 0 && done % a.snap_stride == 0;
+#pragma unroll
+            for (int i = 0; i < TR; ++i) {
+                float4 *p = reinterpret_cast<float4 *>(sm.S + (sr + i) * LK + sc);
+                float4 x = *p;
+                x.x = fmaf(d.x, x.x, fmaf(d.y, x.x, acc[i][0]));
+                x.y = fmaf(d.x, x.y, fmaf(d.y, x.y, acc[i][1]));
+                x.z = fmaf(d.x, x.z, fmaf(d.y, x.z, acc[i][2]));
+                x.w = fmaf(d.x, x.w, fmaf(d.y, x.w, acc[i][3]));
+                *p = x;
+                if (snap)
+                    *reinterpret_cast<float4 *>(
+                        a.snaps + (((s.n * a.n_snap + done / a.snap_stride - 1) * a.H + h) * dv + r0 + sr + i) * DK + sc) = x;
+            }
+        }
+    }
+    if (a.final_state && s.j == s.nseg - 1) {  // (each thread stores what it alone wrote)
+        float *to = a.final_state + (s.n * a.H + h) * dv * DK;
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+            *reinterpret_cast<float4 *>(to + (int64_t)(r0 + sr + i) * DK + sc) =
+                *reinterpret_cast<const float4 *>(sm.S + (sr + i) * LK + sc);
+    }
+}
+
+// U of one segment (not its sequence's last), head and 32 value channels, and the
+// segment's decay.  From the last chunk backwards, so that every weight is the sum of
+// the gates after its token; it ends where nothing before could reach the segment's end.
+template <int DK, typename Tin>
+__global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a, int64_t dv, bool fixed) {
+    constexpr int LK = DK + 4, LV = kRows + 4, TR = DK / 32;
+    __shared__ __align__(16) float ks[kC * LK];
+    __shared__ __align__(16) float vs[kC * LV];
+    __shared__ float ws[kC];
+    __shared__ float s_total;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slices = (int)(dv / kRows);
+    const int64_t id = blockIdx.x;
+    const int64_t h = id / slices % a.H;
+    const int r0 = (int)(id % slices) * kRows;
+    Slot s;
+    if (!locate<true>(a, id / slices / a.H, s) || s.nseg < 2 || s.j == s.nseg - 1) return;
+    const int64_t hq = h / (a.H / a.Hk);
+    const Tin *k = static_cast<const Tin *>(a.k) + (s.start * a.Hk + hq) * DK;
+    const Tin *v = static_cast<const Tin *>(a.v) + (s.start * a.H + h) * dv + r0;
+    const int64_t ldk = a.Hk * DK, ldv = a.H * dv;
+    const int sc = tid % (DK / 4) * 4, sr = tid / (DK / 4) * TR;
+    float acc[TR][4] = {};
+    float after_chunk = 0.f;  // sum of the gates after the chunk
+    for (int64_t t0 = s.len - kC; t0 >= 0 && after_chunk > kDead; t0 -= kC) {  // (segments here are whole chunks)
+        __syncthreads();
+        stage_rows<DK, LK>(ks, k + t0 * ldk, ldk, kC);
+        stage_rows<kRows, LV>(vs, v + t0 * ldv, ldv, kC);
+        if (warp == 0) {
+            const float g = gate2(a, fixed, s.start + t0 + lane, h);
+            float G, after;
+            warp_scans(g, lane, G, after);
+            ws[lane] = ex2(after + after_chunk);
+            if (lane == 31) s_total = G;
+        }
+        __syncthreads();
+        after_chunk += s_total;
+        for (int j = 0; j < kC; ++j) {
+            const float4 kk = *reinterpret_cast<const float4 *>(ks + j * LK + sc);
+            const float w = ws[j];
+#pragma unroll
+            for (int i = 0; i < TR; ++i) {
+                const float x = w * vs[j * LV + sr + i];
+                acc[i][0] = fmaf(x, kk.x, acc[i][0]);
+                acc[i][1] = fmaf(x, kk.y, acc[i][1]);
+                acc[i][2] = fmaf(x, kk.z, acc[i][2]);
+                acc[i][3] = fmaf(x, kk.w, acc[i][3]);
+            }
+        }
+    }
+    float *U = a.states + (s.ss * a.H + h) * dv * DK;
+#pragma unroll
+    for (int i = 0; i < TR; ++i)
+        *reinterpret_cast<float4 *>(U + (int64_t)(r0 + sr + i) * DK + sc) =
+            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    // the segment's decay (once it is past kDead, how far past does not matter)
+    if (r0 == 0 && tid == 0)
+        a.tot[s.ss * a.H + h] = fixed ? (double)a.g[h] * 1.4426950408889634074 * (double)s.len : (double)after_chunk;
+}
+
+// Start states of the segments of one sequence and head, in place of their U:
+// S_{j+1} = 2^{tot_j} S_j + U_j.  A thread chains four elements; the next U is in flight
+// while the current one is added.
+constexpr int kCombThreads = 256;
+__global__ void __launch_bounds__(kCombThreads) gdn_linattn_combine(const Args a, int64_t elems) {
+    const int64_t h = blockIdx.y, e = ((int64_t)blockIdx.z * kCombThreads + threadIdx.x) * 4;
+    if (e >= elems) return;
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+        int64_t start, len;
+        seq_bounds(a.cu, n, a.T, a.rows, start, len);
+        const int64_t nseg = (len + a.seg - 1) / a.seg, ss = state_base(a, n);
+        if (nseg < 2 || ss + nseg > a.sslots) continue;
+        float4 S = a.h0 ? *reinterpret_cast<const float4 *>(a.h0 + (n * a.H + h) * elems + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float *p = a.states + (ss * a.H + h) * elems + e;
+        const double *tot = a.tot + ss * a.H + h;
+        const int64_t step = a.H * elems;
+        float4 u = *reinterpret_cast<const float4 *>(p);
+        for (int64_t j = 0; j + 1 < nseg; ++j) {
+            float4 next = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j + 2 < nseg) next = *reinterpret_cast<const float4 *>(p + step);
+            const float2 d = exp2_pair(tot[j * a.H]);
+            *reinterpret_cast<float4 *>(p) = S;
+            S.x = fmaf(d.x, S.x, fmaf(d.y, S.x, u.x));
+            S.y = fmaf(d.x, S.y, fmaf(d.y, S.y, u.y));
+            S.z = fmaf(d.x, S.z, fmaf(d.y, S.z, u.z));
+            S.w = fmaf(d.x, S.w, fmaf(d.y, S.w, u.w));
+            u = next;
+            p += step;
+        }
+        *reinterpret_cast<float4 *>(p) = S;
+    }
+}
+
+template <int DK, typename Tin>
+gdn_status launch_dk(const Plan &p, const Args &a, cudaStream_t s) {
+    const int64_t slices = p.dv / kRows, grid = p.slots * p.H * slices, sgrid = p.sslots * p.H * slices;
+    if (grid > 0x7fffffffLL || sgrid > 0x7fffffffLL) return fail(GDN_ERR_UNSUPPORTED, "grid too large");
+    constexpr size_t smem = sizeof(Smem<DK>);
+    static const cudaError_t attr = cudaFuncSetAttribute(gdn_linattn_simt<DK, Tin>,
+                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (attr != cudaSuccess) return fail(GDN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(attr));
+    gdn_status st = GDN_OK;
+    if (sgrid > 0) {
+        {
+            log_launch("gdn_linattn_state_simt", dim3((unsigned)sgrid), dim3(kThreads), 0);
+            LaunchScope ls("gdn_linattn_state_simt", s);
+            gdn_linattn_state_simt<DK, Tin><<<(unsigned)sgrid, kThreads, 0, s>>>(a, p.dv, p.fixed_gate);
+        }
+        if ((st = check_launch("gdn_linattn_state_simt")) != GDN_OK) return st;
+        if ((st = launch_combine(p, a, s)) != GDN_OK) return st;
+    }
+    {
+        log_launch("gdn_linattn_simt", dim3((unsigned)grid), dim3(kThreads), smem);
+        LaunchScope ls("gdn_linattn_simt", s);
+        gdn_linattn_simt<DK, Tin><<<(unsigned)grid, kThreads, smem, s>>>(a, p.dv, p.fixed_gate);
+    }
+    return check_launch("gdn_linattn_simt");
+}
+
+}  // namespace
+
+gdn_status launch_combine(const Plan &p, const Args &a, cudaStream_t s) {
+    if (p.H > 65535) return fail(GDN_ERR_UNSUPPORTED, "more than 65535 heads");
+    const int64_t elems = p.dv * p.dk;
+    const dim3 grid((unsigned)(p.N < 64 ? p.N : 64), (unsigned)p.H,
+                    (unsigned)((elems + 4 * kCombThreads - 1) / (4 * kCombThreads)));
+    log_launch("gdn_linattn_combine", grid, dim3(kCombThreads), 0);
+    LaunchScope ls("gdn_linattn_combine", s);
+    gdn_linattn_combine<<<grid, kCombThreads, 0, s>>>(a, elems);
+    return check_launch("gdn_linattn_combine");
+}
+
+gdn_status launch_simt(const Plan &p, const Args &a, int dtype, cudaStream_t s) {
+    if (dtype == GDN_BF16)
+        return p.dk == 128 ? launch_dk<128, __nv_bfloat16>(p, a, s) : launch_dk<64, __nv_bfloat16>(p, a, s);
+    return p.dk == 128 ? launch_dk<128, float>(p, a, s) : launch_dk<64, float>(p, a, s);
+}
+
+}  // namespace lin
+}  // namespace gdn

@@ -6,7 +6,7 @@ when the caller does not pass them, and forwards pointers and the current CUDA
 stream.  There is no CPU fallback: when ``libgdn.so`` is missing or cannot be
 loaded, every call raises.
 
-Names follow the C ABI in ``include/gdn.h``.
+Names follow the C ABI in ``include/gdn.h`` and ``include/gdn_linattn.h``.
 """
 from __future__ import annotations
 
@@ -24,6 +24,7 @@ GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUD
     GDN_ERR_INTERNAL = range(7)
 GDN_F32, GDN_BF16 = 0, 1
 GDN_GATE_HEAD, GDN_GATE_CHANNEL = 0, 1
+GDN_GATE_CONST = 2  # gdn_linattn_* only: one fixed decay per head
 
 GDN_DEV_OK, GDN_DEV_TIMEOUT_PREP, GDN_DEV_TIMEOUT_SCAN, GDN_DEV_BOUNDS = 0, 1, 2, 16
 
@@ -32,11 +33,27 @@ EXPORTED = ("gdn_chunk_workspace_size", "gdn_chunk_fwd", "gdn_chunk_status", "gd
             "gdn_decode_step_prerule", "gdn_status_string", "gdn_last_error", "gdn_profile_enable",
             "gdn_profile_read")
 
+# entry points of include/gdn_linattn.h
+EXPORTED_LINATTN = ("gdn_linattn_workspace_size", "gdn_linattn_chunk_fwd", "gdn_linattn_decode_step",
+                    "gdn_qk_norm_rope", "gdn_beam_workspace_size", "gdn_beam_select", "gdn_state_reorder")
+
 
 class GdnDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64),
                 ("dk", ctypes.c_int64), ("dv", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("gate", ctypes.c_int32), ("scale", ctypes.c_float), ("hk", ctypes.c_int32)]
+
+
+class GdnQkRopeDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("hq", ctypes.c_int32), ("hk", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class GdnBeamDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("W", ctypes.c_int32), ("V", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("row_stride", ctypes.c_int64)]
 
 
 class GdnKernelTime(ctypes.Structure):
@@ -75,6 +92,14 @@ def load_library(path: str = LIB_PATH):
         lib.gdn_state_select.argtypes = [dp, vp, vp, vp, vp]
         lib.gdn_prerule.argtypes = [dp, vp, vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.gdn_decode_step_prerule.argtypes = [dp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+        lib.gdn_linattn_workspace_size.argtypes = [dp, i32, ctypes.POINTER(sz)]
+        lib.gdn_linattn_chunk_fwd.argtypes = [dp, vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, vp, vp, sz, vp]
+        lib.gdn_linattn_decode_step.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp]
+        lib.gdn_qk_norm_rope.argtypes = [ctypes.POINTER(GdnQkRopeDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        bp = ctypes.POINTER(GdnBeamDesc)
+        lib.gdn_beam_workspace_size.argtypes = [bp, ctypes.POINTER(sz)]
+        lib.gdn_beam_select.argtypes = [bp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.gdn_state_reorder.argtypes = [vp, vp, i64, i32, sz, vp]
         lib.gdn_status_string.argtypes = [ctypes.c_int]
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_last_error.argtypes = []
@@ -84,7 +109,7 @@ def load_library(path: str = LIB_PATH):
         for name in ("gdn_chunk_workspace_size", "gdn_chunk_fwd", "gdn_chunk_status", "gdn_chunk_status_static",
                      "gdn_chunk_fwd_static", "gdn_decode_step",
                      "gdn_decode_multi", "gdn_state_select", "gdn_prerule", "gdn_decode_step_prerule",
-                     "gdn_profile_enable", "gdn_profile_read"):
+                     "gdn_profile_enable", "gdn_profile_read") + EXPORTED_LINATTN:
             getattr(lib, name).restype = ctypes.c_int
         if path == LIB_PATH:
             _lib = lib
@@ -321,6 +346,240 @@ def gdn_state_select(step_states, accept, state, *, stream=None):
     d = make_desc(B, T, H, dk, dv, GDN_F32, False, 1.0)
     _check(lib, lib.gdn_state_select(ctypes.byref(d), _ptr(step_states), _ptr(accept), _ptr(state),
                                      _stream(stream)))
+    return state
+
+
+# ---------------------------------------------------------------------------
+# include/gdn_linattn.h: linear attention with a decay for each head, the norm and
+# rotation of queries and keys, beam search over recurrent states
+# ---------------------------------------------------------------------------
+
+class _Launch:
+    """Where a call runs: the device its tensors are on and the stream it is queued on
+    (the current one of that device, or `stream`), also current for what the call allocates."""
+
+    def __init__(self, stream, *ts):
+        ts = [t for t in ts if t is not None]
+        _need_cuda_any(*ts)
+        dev = ts[0].device
+        for t in ts:
+            if t.device != dev:
+                raise ValueError(f"tensors are on different devices: {dev} and {t.device}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+        self.device = dev
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        self._with = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self._with.__enter__()  # makes the stream's device current too
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        return self._with.__exit__(*exc)
+
+
+def _need_cuda_any(*ts):
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors (the library has no CPU path)")
+
+
+def _need(name, t, shape, dtype=None, optional=False):
+    """`t` is a contiguous tensor of `shape` (and `dtype`)."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is required")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def gdn_linattn_workspace_size(B, T, H, dk, dv, num_seqs, *, dtype=torch.bfloat16, hk=0) -> int:
+    lib = load_library()
+    d = make_desc(B, T, H, dk, dv, GDN_F32 if dtype == torch.float32 else GDN_BF16, False, 1.0, hk)
+    n = ctypes.c_size_t(0)
+    _check(lib, lib.gdn_linattn_workspace_size(ctypes.byref(d), int(num_seqs), ctypes.byref(n)))
+    return int(n.value)
+
+
+def gdn_linattn_chunk_fwd(q, k, v, log_gate, initial_state=None, cu_seqlens=None, *, scale=1.0, snapshot_stride=0,
+                          out=None, final_state=True, snapshots=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head over prompts: S_t = exp(g_t) S_{t-1} + v_t k_t^T,
+    o_t = S_t (scale q_t).  Shapes as gdn_chunk_fwd; log_gate (B,T,H), or (H,) for one fixed decay per head.
+    final_state: True to allocate, a tensor to fill (may be initial_state), or None.
+    Returns (out, final_state, snapshots).  gdn_chunk_status(workspace) reads the call's device status."""
+    lib = load_library()
+    B, T, Hq, dk = q.shape
+    H, dv = v.shape[-2], v.shape[-1]
+    N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else B
+    code = _dtype_code(q)
+    _need("q", q, (B, T, Hq, dk))
+    _need("k", k, (B, T, Hq, dk), q.dtype)
+    _need("v", v, (B, T, H, dv), q.dtype)
+    fixed = log_gate.dim() == 1
+    _need("log_gate", log_gate, (H,) if fixed else (B, T, H), torch.float32)
+    _need("initial_state", initial_state, (N, H, dv, dk), torch.float32, optional=True)
+    _need("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, optional=True)
+    given = [t for t in (out, final_state, snapshots, workspace) if isinstance(t, torch.Tensor)]
+    with (at := _Launch(stream, q, k, v, log_gate, initial_state, cu_seqlens, *given)) as s:
+        if out is None:
+            out = torch.empty((B, T, H, dv), dtype=q.dtype, device=at.device)
+        if final_state is True:
+            final_state = torch.empty((N, H, dv, dk), dtype=torch.float32, device=at.device)
+        elif final_state is False:
+            final_state = None
+        if snapshot_stride > 0 and snapshots is None:
+            snapshots = torch.empty((B, T // snapshot_stride, H, dv, dk), dtype=torch.float32, device=at.device)
+        _need("out", out, (B, T, H, dv), q.dtype)
+        _need("final_state", final_state, (N, H, dv, dk), torch.float32, optional=True)
+        if snapshot_stride > 0:
+            _need("snapshots", snapshots, (B, T // snapshot_stride, H, dv, dk), torch.float32)
+        d = make_desc(B, T, H, dk, dv, code, False, scale, Hq)
+        d.gate = GDN_GATE_CONST if fixed else GDN_GATE_HEAD
+        if workspace is None:
+            n = ctypes.c_size_t(0)
+            _check(lib, lib.gdn_linattn_workspace_size(ctypes.byref(d), int(N), ctypes.byref(n)))
+            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=at.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        _check(lib, lib.gdn_linattn_chunk_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate),
+                                              _ptr(initial_state), _ptr(cu_seqlens), int(N), int(snapshot_stride),
+                                              _ptr(out), _ptr(final_state), _ptr(snapshots), _ptr(workspace),
+                                              workspace.numel() * workspace.element_size(), s))
+    return out, final_state, snapshots
+
+
+def gdn_linattn_decode_step(q, k, v, log_gate, state, *, scale=1.0, out=None, stream=None):
+    """One token of every live sequence of gdn_linattn_chunk_fwd's recurrence; `state` (B,H,dv,dk) fp32 is
+    updated in place.  q, k (B,1,hk,dk) or (B,hk,dk); v (B,1,H,dv) or (B,H,dv); log_gate (B,[1,]H) or (H,)."""
+    lib = load_library()
+    B, H, dv, dk = state.shape
+    hk = q.shape[-2]
+    code = _dtype_code(q)
+    lead = (B,) if q.dim() == 3 else (B, 1)
+    _need("q", q, lead + (hk, dk))
+    _need("k", k, lead + (hk, dk), q.dtype)
+    _need("v", v, ((B,) if v.dim() == 3 else (B, 1)) + (H, dv), q.dtype)
+    fixed = log_gate.dim() == 1
+    _need("log_gate", log_gate, (H,) if fixed else ((B,) if log_gate.dim() == 2 else (B, 1)) + (H,), torch.float32)
+    _need("state", state, (B, H, dv, dk), torch.float32)
+    with (at := _Launch(stream, q, k, v, log_gate, state, out)) as s:
+        if out is None:
+            out = torch.empty((B, 1, H, dv), dtype=q.dtype, device=at.device)
+        if out.numel() != B * H * dv or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous (B, 1, H, dv) tensor of {q.dtype}")
+        d = make_desc(B, 1, H, dk, dv, code, False, scale, hk)
+        d.gate = GDN_GATE_CONST if fixed else GDN_GATE_HEAD
+        _check(lib, lib.gdn_linattn_decode_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate),
+                                                _ptr(state), _ptr(out), s))
+    return out
+
+
+def _token_rows(name, x):
+    """(B, T, heads, d) with a token's heads side by side and tokens evenly spaced: the elements from one
+    token to the next.  Slices of a wider projection have that form; anything else is refused."""
+    B, T, h, d = x.shape
+    st = x.stride()
+    if (d > 1 and st[3] != 1) or (h > 1 and st[2] != d):
+        raise ValueError(f"{name}: a token's heads must lie side by side")
+    if B * T <= 1:
+        return h * d
+    if T > 1:
+        if B > 1 and st[0] != T * st[1]:
+            raise ValueError(f"{name}: tokens must be evenly spaced over (B, T)")
+        return st[1]
+    return st[0]
+
+
+def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, *, eps=1e-6, weight_offset=0.0,
+                     interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norm of every query and key head (over its channels, times weight_offset + weight) and the position
+    rotation, in one pass.  q (B,T,hq,d), k (B,T,hk,d): dense, or slices of a wider projection (a token's
+    heads side by side); positions (B,T) int32; inv_freq (rot/2,) fp32, or None: no rotation; the weights (d,)
+    fp32 or None.  Pairs are (i, i + rot/2), or (2i, 2i+1) when `interleaved`.  Returns (q_out, k_out), dense;
+    either may be its (dense) input."""
+    lib = load_library()
+    B, T, hq, dim = q.shape
+    hk = k.shape[2]
+    code = _dtype_code(q)
+    if k.dtype != q.dtype or tuple(k.shape) != (B, T, hk, dim):
+        raise ValueError(f"k must be {(B, T, hk, dim)} of {q.dtype}, got {tuple(k.shape)} of {k.dtype}")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot:
+        _need("inv_freq", inv_freq, (rot // 2,), torch.float32)
+        _need("positions", positions, (B, T), torch.int32)
+    _need("q_weight", q_weight, (dim,), torch.float32, optional=True)
+    _need("k_weight", k_weight, (dim,), torch.float32, optional=True)
+    used = [q, k, positions if rot else None, inv_freq, q_weight, k_weight, q_out, k_out]
+    with (at := _Launch(stream, *used)) as s:
+        if q_out is None:
+            q_out = torch.empty((B, T, hq, dim), dtype=q.dtype, device=at.device)
+        if k_out is None:
+            k_out = torch.empty((B, T, hk, dim), dtype=q.dtype, device=at.device)
+        _need("q_out", q_out, (B, T, hq, dim), q.dtype)
+        _need("k_out", k_out, (B, T, hk, dim), q.dtype)
+        d = GdnQkRopeDesc(B * T, hq, hk, dim, rot, 1 if interleaved else 0, code, _token_rows("q", q),
+                          _token_rows("k", k) if hk else 0, float(eps), float(weight_offset))
+        _check(lib, lib.gdn_qk_norm_rope(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(positions if rot else None),
+                                         _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out), s))
+    return q_out, k_out
+
+
+def gdn_beam_select(logits, scores, K, *, out_scores=None, out_parent=None, out_token=None, workspace=None,
+                    stream=None):
+    """One step of beam search: for each request the K best of its W x V continuations by
+    scores[b, w] + log_softmax(logits[b, w])[t], best first, equals in index order.
+    logits (B,W,V) fp32 or bf16 (rows of V values evenly spaced: a padded vocabulary may be sliced off);
+    scores (B,W) fp32 or None (zeros).  Returns (scores (B,K) fp32, parent beam (B,K) int32, token (B,K) int32)."""
+    lib = load_library()
+    B, W, V = logits.shape
+    code = _dtype_code(logits)
+    st = logits.stride()
+    if V > 1 and st[2] != 1:
+        raise ValueError("logits: a row's values must be contiguous")
+    if B > 1 and W > 1 and st[0] != W * st[1]:
+        raise ValueError("logits: rows must be evenly spaced over (B, W)")
+    stride = V if B * W <= 1 else (st[1] if W > 1 else st[0])
+    _need("scores", scores, (B, W), torch.float32, optional=True)
+    with (at := _Launch(stream, logits, scores, out_scores, out_parent, out_token, workspace)) as s:
+        new = lambda dt: torch.empty((B, K), dtype=dt, device=at.device)  # noqa: E731
+        out_scores = new(torch.float32) if out_scores is None else out_scores
+        out_parent = new(torch.int32) if out_parent is None else out_parent
+        out_token = new(torch.int32) if out_token is None else out_token
+        _need("out_scores", out_scores, (B, K), torch.float32)
+        _need("out_parent", out_parent, (B, K), torch.int32)
+        _need("out_token", out_token, (B, K), torch.int32)
+        d = GdnBeamDesc(B, W, V, int(K), code, stride)
+        if workspace is None:
+            n = ctypes.c_size_t(0)
+            _check(lib, lib.gdn_beam_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=at.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        _check(lib, lib.gdn_beam_select(ctypes.byref(d), _ptr(logits), _ptr(scores), _ptr(out_scores),
+                                        _ptr(out_parent), _ptr(out_token), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), s))
+    return out_scores, out_parent, out_token
+
+
+def gdn_state_reorder(state, parent, *, stream=None):
+    """Move per-beam states to the beams that go on with them, in place: state row (b, w) becomes row
+    (b, parent[b, w]) as it was before the call; a parent outside 0 .. W-1 leaves its row.  `state`: a
+    contiguous tensor of any type whose leading dimension is B * W (recurrent states, convolution histories;
+    a row is a multiple of 16 bytes); parent (B, W) int32.  Returns state."""
+    lib = load_library()
+    B, W = parent.shape
+    _need("parent", parent, (B, W), torch.int32)
+    if state.dim() < 1 or state.shape[0] != B * W or not state.is_contiguous():
+        raise ValueError(f"state must be contiguous with {B * W} rows")
+    row_bytes = state.numel() // max(B * W, 1) * state.element_size()
+    with _Launch(stream, state, parent) as s:
+        _check(lib, lib.gdn_state_reorder(_ptr(state), _ptr(parent), int(B), int(W), int(row_bytes), s))
     return state
 
 
