@@ -64,7 +64,8 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
     p.dv = d.dv;
     p.packed = packed;
     p.fixed_gate = d.gate == GDN_GATE_CONST;
-    p.tc = false;
+    // bf16 with 128-wide heads on the tensor cores, all else on the CUDA cores
+    p.tc = d.dtype == GDN_BF16 && d.dk == 128 && d.dv == 128;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
@@ -198,7 +199,7 @@ gdn_status gdn_linattn_chunk_fwd(const gdn_desc *d, const void *q, const void *k
     a.snaps = snapshots;
     a.tot = reinterpret_cast<double *>(ws + p.off_tot);
     a.states = reinterpret_cast<float *>(ws + p.off_state);
-    return launch_simt(p, a, d->dtype, (cudaStream_t)stream);
+    return p.tc ? launch_tc(p, a, (cudaStream_t)stream) : launch_simt(p, a, d->dtype, (cudaStream_t)stream);
 }
 
 gdn_status gdn_linattn_decode_step(const gdn_desc *d, const void *q, const void *k, const void *v,
