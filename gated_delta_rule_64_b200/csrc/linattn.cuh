@@ -34,7 +34,8 @@ struct Plan {
     int64_t G;       // fixed-length sequences: segments per sequence (>= 1)
     int64_t slots;   // segments in all (packed: an upper bound)
     int64_t sslots;  // segments of sequences that have more than one (packed: an upper bound; 0: none has)
-    size_t off_status, off_tot, off_state, total;
+    int64_t parts, part_len;  // blocks of the state kernel per segment, and their tokens
+    size_t off_status, off_tot, off_alive, off_state, total;
 };
 Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed);
 
@@ -42,13 +43,14 @@ struct Args {
     const void *q, *k, *v;
     const float *g, *h0;
     const int32_t *cu;
-    int64_t T, N, rows, H, Hk, seg, G, slots, sslots;
+    int64_t T, N, rows, H, Hk, seg, G, slots, sslots, parts, part_len;
     float scale;
     int64_t snap_stride, n_snap;
     void *out;
     float *final_state, *snaps;
     double *tot;     // [sslots][H] decay of a segment, log2 units
-    float *states;   // [sslots][H][d_v][d_k]: U of a segment, then its start state
+    int32_t *alive;  // [sslots][parts][H] 1: the part's U was formed (0: it is zero)
+    float *states;   // [sslots][parts][H][d_v][d_k]: U of a part; part 0: then the segment's start state
     int *status;
 };
 

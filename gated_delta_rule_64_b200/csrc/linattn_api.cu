@@ -83,13 +83,20 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
         p.slots = p.N * p.G;
         p.sslots = p.G > 1 ? p.slots : 0;
     }
+    // Parts of a segment's state (tensor cores): at most eight, of 16 chunks or more.  The
+    // CUDA-core state kernel takes a segment whole (it has d_v / 32 blocks for it already).
+    const int64_t chunks = p.seg / kChunk;
+    p.parts = p.tc ? (chunks / 16 < 1 ? 1 : (chunks / 16 > 8 ? 8 : chunks / 16)) : 1;
+    p.part_len = (chunks + p.parts - 1) / p.parts * kChunk;
     size_t off = 0;
     p.off_status = off;
     off += kStatusBytes;
     p.off_tot = off;
     off = align_up(off + sizeof(double) * (size_t)p.sslots * p.H, 256);
+    p.off_alive = off;
+    off = align_up(off + sizeof(int32_t) * (size_t)p.sslots * p.parts * p.H, 256);
     p.off_state = off;
-    off += sizeof(float) * (size_t)p.sslots * p.H * p.dv * p.dk;
+    off += sizeof(float) * (size_t)p.sslots * p.parts * p.H * p.dv * p.dk;
     p.total = align_up(off, 256);
     return p;
 }
@@ -191,6 +198,8 @@ gdn_status gdn_linattn_chunk_fwd(const gdn_desc *d, const void *q, const void *k
     a.G = p.G;
     a.slots = p.slots;
     a.sslots = p.sslots;
+    a.parts = p.parts;
+    a.part_len = p.part_len;
     a.scale = d->scale;
     a.snap_stride = snapshot_stride;
     a.n_snap = n_snap;
@@ -198,6 +207,7 @@ gdn_status gdn_linattn_chunk_fwd(const gdn_desc *d, const void *q, const void *k
     a.final_state = final_state;
     a.snaps = snapshots;
     a.tot = reinterpret_cast<double *>(ws + p.off_tot);
+    a.alive = reinterpret_cast<int32_t *>(ws + p.off_alive);
     a.states = reinterpret_cast<float *>(ws + p.off_state);
     return p.tc ? launch_tc(p, a, (cudaStream_t)stream) : launch_simt(p, a, d->dtype, (cudaStream_t)stream);
 }

@@ -278,13 +278,15 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a,
         *reinterpret_cast<float4 *>(U + (int64_t)(r0 + sr + i) * DK + sc) =
             make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     // the segment's decay (once it is past kDead, how far past does not matter)
-    if (r0 == 0 && tid == 0)
+    if (r0 == 0 && tid == 0) {
+        a.alive[s.ss * a.H + h] = 1;
         a.tot[s.ss * a.H + h] = fixed ? (double)a.g[h] * 1.4426950408889634074 * (double)s.len : (double)after_chunk;
+    }
 }
 
-// Start states of the segments of one sequence and head, in place of their U:
-// S_{j+1} = 2^{tot_j} S_j + U_j.  A thread chains four elements; the next U is in flight
-// while the current one is added.
+// Start states of the segments of one sequence and head, each in the place of its first
+// part's U: S_{j+1} = 2^{tot_j} S_j + sum of the parts' U_j.  A thread chains four
+// elements; the next segment's U are in flight while the current one is added.
 constexpr int kCombThreads = 256;
 __global__ void __launch_bounds__(kCombThreads) gdn_linattn_combine(const Args a, int64_t elems) {
     const int64_t h = blockIdx.y, e = ((int64_t)blockIdx.z * kCombThreads + threadIdx.x) * 4;
@@ -294,24 +296,33 @@ __global__ void __launch_bounds__(kCombThreads) gdn_linattn_combine(const Args a
         seq_bounds(a.cu, n, a.T, a.rows, start, len);
         const int64_t nseg = (len + a.seg - 1) / a.seg, ss = state_base(a, n);
         if (nseg < 2 || ss + nseg > a.sslots) continue;
-        float4 S = a.h0 ? *reinterpret_cast<const float4 *>(a.h0 + (n * a.H + h) * elems + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float *p = a.states + (ss * a.H + h) * elems + e;
+        const int parts = (int)a.parts;
+        float *states = a.states + (ss * parts * a.H + h) * elems + e;
+        const int32_t *alive = a.alive + ss * parts * a.H + h;
         const double *tot = a.tot + ss * a.H + h;
-        const int64_t step = a.H * elems;
-        float4 u = *reinterpret_cast<const float4 *>(p);
+        auto added = [&](int64_t j) {
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int i = 0; i < parts; ++i)
+                if (alive[(j * parts + i) * a.H]) {
+                    const float4 x = *reinterpret_cast<const float4 *>(states + (j * parts + i) * a.H * elems);
+                    u.x += x.x; u.y += x.y; u.z += x.z; u.w += x.w;
+                }
+            return u;
+        };
+        float4 S = a.h0 ? *reinterpret_cast<const float4 *>(a.h0 + (n * a.H + h) * elems + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 u = added(0);
         for (int64_t j = 0; j + 1 < nseg; ++j) {
-            float4 next = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j + 2 < nseg) next = *reinterpret_cast<const float4 *>(p + step);
+            const float4 next = j + 2 < nseg ? added(j + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
             const float2 d = exp2_pair(tot[j * a.H]);
-            *reinterpret_cast<float4 *>(p) = S;
+            *reinterpret_cast<float4 *>(states + j * parts * a.H * elems) = S;
             S.x = fmaf(d.x, S.x, fmaf(d.y, S.x, u.x));
             S.y = fmaf(d.x, S.y, fmaf(d.y, S.y, u.y));
             S.z = fmaf(d.x, S.z, fmaf(d.y, S.z, u.z));
             S.w = fmaf(d.x, S.w, fmaf(d.y, S.w, u.w));
             u = next;
-            p += step;
         }
-        *reinterpret_cast<float4 *>(p) = S;
+        *reinterpret_cast<float4 *>(states + (nseg - 1) * parts * a.H * elems) = S;
     }
 }
 

@@ -3,32 +3,40 @@
 // the top of linattn.cuh; chunks have 64 tokens.  Per chunk the output kernel forms, with
 // fp32 accumulators in TMEM and the 128 value channels as MMA rows,
 //
-//     QK  = Q K^T                     64 x 64 (a 128-row product, its upper half unused)
-//     D1  = S0 Q^T                    128 x 64: what the state before the chunk gives
-//     D2  = V^T P^T                   128 x 64: what the chunk's own tokens give
+//     QK  = Q K^T                     64 x 64
+//     O   = S0 Q^T + V^T P^T          128 x 64 (one accumulator)
 //     dS  = (V w)^T K                 128 x 128: the state's increment
 //
-// with P_ij = scale 2^{G_i - G_j} QK_ij for j <= i and w_j = 2^{G - G_j}, then
-// o_i = scale 2^{G_i} D1_i + D2_i and S = 2^G S0 + dS.
+// with P_ij = 2^{-G_j} QK_ij for j <= i and w_j = 2^{G - G_j}; then o_i = scale 2^{G_i} O_i
+// and S = 2^G S0 + dS.  Where the chunk's decay G is below 2^-100 the factors 2^{-G_j} would
+// leave the range: there P_ij = scale 2^{G_i - G_j} QK_ij, and the Q that S0 multiplies is
+// scaled by scale 2^{G_i} in place (one more rounding to bf16, of that product only).
 //
-// Rounding.  P and the copy of S0 that D1 multiplies are rounded to bf16, once each,
+// Rounding.  P and the copy of S0 that Q multiplies are rounded to bf16, once each,
 // like the output they go into.  The state itself keeps fp32: V w is split into three
 // bf16 terms (8 + 8 + 8 bits: the whole fp32 product) whose products with K add up in the
 // fp32 accumulator, at the price of two more 128 x 128 x 64 products per chunk; one bf16
 // term would leave the state with 2^-9 relative error.
 //
-// Nothing in a chunk but D1 waits for the chunk before it, so the roles run
-// ahead of one another, joined by mbarriers:
-//   warps 0-7    hold the state (two threads per row, 64 columns each): S0 as the bf16
-//                A operand in TMEM, S = 2^G S0 + dS, and the outputs
-//   warps 8-11   the gates' sums, the three terms of V w (shared memory, in the V
-//                tile's own swizzled layout), P
-//   warp 12      TMA loads, three chunks deep (48 KB each)
-//   warp 13      issues the MMAs
-// One block per SM: 201 KB of shared memory, all 512 TMEM columns.
+// The roles run ahead of one another, joined by mbarriers:
+//   warps 0-7    hold the state (two threads per row, 64 columns each): S = 2^G S0 + dS, its
+//                bf16 copy as the A operand of S0 Q^T in TMEM, and the outputs
+//   warps 8-11   the three terms of V w, 32 value channels a warp, as the A operand of dS in
+//                TMEM (two buffers): transposed on the way from shared memory (ldmatrix)
+//                into the fragment layout that a 16-lane TMEM store takes
+//   warps 12-14  P, 16 query tokens a warp (a 64-row product leaves 16 rows in each TMEM
+//   and 15       quarter), through the fragment layout too: TMEM to stmatrix; warp 12, whose
+//                tokens have the fewest keys, also forms the factors that come from the gates
+//   warp 16      issues the TMA loads (three stages of 48 KB) and the MMAs
+// One block per SM: 205 KB of shared memory, all 512 TMEM columns.
 //
-// A chunk moves 64 KB (q, k, v, out): 1.5 us of an SM's share of the HBM bandwidth; its MMAs
-// take about 1400 cycles (0.75 us).
+// The loops of the roles are kept short on purpose: every scheduler runs a warp of each, and
+// with them unrolled (about 40 KB of code) the instruction caches, not the tensor pipe, set
+// the pace: 2.9 us a chunk, 0.36 instructions issued per cycle and scheduler.
+//
+// A chunk moves 64 KB (q, k, v, out): 1.5 us of an SM's share of the HBM bandwidth.  Its MMAs
+// take about 1800 cycles (measured alone: 37 cycles for 128 x 64 x 16 with A in TMEM, 54 with
+// A in shared memory, 69 for 128 x 128 x 16).
 #include <cudaTypedefs.h>
 #include <string.h>
 
@@ -59,17 +67,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
-// 4 x 4 transpose of bf16 values among the 4 lanes of a quad: lane j holds row j as two
-// packed pairs (low half first) and afterwards column j.
-__device__ __forceinline__ void quad_transpose(uint32_t &p01, uint32_t &p23, int lane) {
-    const bool b1 = lane & 2, b0 = lane & 1;
-    const uint32_t r = __shfl_xor_sync(0xffffffffu, b1 ? p01 : p23, 2);
-    const uint32_t a = b1 ? r : p01, b = b1 ? p23 : r;
-    const uint32_t x = __shfl_xor_sync(0xffffffffu, __byte_perm(a, b, b0 ? 0x5410u : 0x7632u), 1);
-    p01 = __byte_perm(a, x, b0 ? 0x3254u : 0x5410u);
-    p23 = __byte_perm(b, x, b0 ? 0x3276u : 0x7610u);
-}
-
 // The gates of a chunk's 64 tokens, two per lane (tokens 2 l, 2 l + 1), in log2 units:
 // G their prefix sums, after the sums of what follows them, total the sum of all.
 __device__ __forceinline__ void scan_gates(float g0, float g1, int lane, float2 &G, float2 &after, float &total) {
@@ -89,49 +86,120 @@ __device__ __forceinline__ void scan_gates(float g0, float g1, int lane, float2 
     total = __shfl_sync(0xffffffffu, up, 31);
 }
 
-// Eight bf16 values times w as three bf16 terms each, x = t0 + t1 + t2 to fp32 precision.
-__device__ __forceinline__ void split_terms(const uint4 &src, float w, uint4 (&t)[3]) {
-    const uint32_t in[4] = {src.x, src.y, src.z, src.w};
-    uint32_t o[3][4];
+// Fragments: a 16 x 8k block over a warp, lane l holding rows l / 4 and l / 4 + 8.
+// Store of 16 TMEM lanes: repeat n covers columns 4 n .. 4 n + 3, lane l's word of column
+// 4 n + l % 4 of row l / 4 in r[2 n], of row l / 4 + 8 in r[2 n + 1].
+// Over 8 columns.
+__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// Load of 16 TMEM lanes: lane l holds columns 8 n + 2 (l % 4), + 1 of row l / 4 in
+// x[4 n], x[4 n + 1], of row l / 4 + 8 in x[4 n + 2], x[4 n + 3].  Over 16 columns,
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, float (&x)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 x = __fmul2_rn(make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)),
-                              make_float2(w, w));
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+}
+// over 32 columns.
+__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, float (&x)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            o[k][i] = pack_bf16(x.x, x.y);
-            if (k < 2)
-                x = __fadd2_rn(x, make_float2(-__uint_as_float(o[k][i] << 16), -__uint_as_float(o[k][i] & 0xffff0000u)));
-        }
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+// Four 8 x 8 b16 matrices, transposed: lanes 8 m .. 8 m + 7 give the row addresses of
+// matrix m; lane l receives (column l / 4, rows 2 (l % 4), + 1) of it in r[m].
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+// Two bf16 values (low half first) times their weights, cut into three bf16 pairs whose sum is the
+// fp32 product exactly: 24 significant bits are eight, eight and eight, each cut off.
+__device__ __forceinline__ void split_terms(uint32_t v, float2 w, uint32_t &t0, uint32_t &t1, uint32_t &t2) {
+    const float2 x = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), w);
+    const uint32_t x0 = __float_as_uint(x.x), x1 = __float_as_uint(x.y);
+    t0 = __byte_perm(x0, x1, 0x7632);
+    const float2 y = __fadd2_rn(x, make_float2(-__uint_as_float(x0 & 0xffff0000u), -__uint_as_float(x1 & 0xffff0000u)));
+    const uint32_t y0 = __float_as_uint(y.x), y1 = __float_as_uint(y.y);
+    t1 = __byte_perm(y0, y1, 0x7632);
+    const float2 z = __fadd2_rn(y, make_float2(-__uint_as_float(y0 & 0xffff0000u), -__uint_as_float(y1 & 0xffff0000u)));
+    t2 = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
+}
+
+// The three terms of V w for 16 value channels and 16 tokens, in the fragment layout of the
+// TMEM stores.  addr: this lane's row for ldmatrix, of the matrices (tokens, channels) = (0-7,
+// 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15); w: the tokens' weights.
+__device__ __forceinline__ void channel_terms(uint32_t addr, const float *w, int lane, uint32_t (&t0)[4], uint32_t (&t1)[4],
+                                              uint32_t (&t2)[4]) {
+    uint32_t r[4];
+    ldsm_x4_trans(addr, r);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const float2 f = *reinterpret_cast<const float2 *>(w + 8 * m + 2 * (lane & 3));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) split_terms(r[2 * m + e], f, t0[2 * m + e], t1[2 * m + e], t2[2 * m + e]);
     }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) t[k] = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+}
+// That lane's row address for tokens `first` .. of a V half tile (64 channels) and the channels
+// from 16-byte piece `piece` on (first: a multiple of 8).
+__device__ __forceinline__ uint32_t terms_address(uint32_t half, int piece, int first, int lane) {
+    const int row = first + (lane & 7) + ((lane >> 4) << 3), p = piece + ((lane >> 3) & 1);
+    return half + (uint32_t)row * 128u + (((uint32_t)p ^ (uint32_t)(row & 7)) << 4);
 }
 
 // ===========================================================================
 // Output kernel
 // ===========================================================================
 // A stage: [Q, channels 0-63][K, 0-63][Q, 64-127][K, 64-127][V, 0-63][V, 64-127], each 64
-// token rows of 128 bytes (128-byte swizzle); K follows Q so that the 128-row A operand of
-// QK stays inside the stage.
+// token rows of 128 bytes (128-byte swizzle).
 constexpr uint32_t kStQ = 0, kStK = 8192, kStV = 32768, kHalfQK = 16384, kHalfV = 8192, kStage = 49152;
 constexpr int kStages = 3;
-constexpr uint32_t kOffT = kStages * kStage;   // the three terms of V w, 16 KB each
-constexpr uint32_t kOffP = kOffT + 3 * 16384;  // P, 64 rows of 128 bytes
-constexpr uint32_t kOutSmem = kOffP + 8192 + 1024;
-constexpr uint32_t kTmQK = 0, kTmD1 = 64, kTmD2 = 192, kTmS = 320, kTmA = 448;  // D1, D2: two buffers each
-constexpr int kOutThreads = 14 * 32;
-constexpr int kRing = 4;
+constexpr uint32_t kOffP = kStages * kStage;   // P, 64 rows of 128 bytes; two buffers
+constexpr uint32_t kOffO = kOffP + 2 * 8192;   // outputs, 64 rows of 256 bytes (16-byte pieces turned by row); two buffers
+constexpr uint32_t kOutSmem = kOffO + 2 * 16384 + 1024;
+// TMEM columns: QK, O, dS, S0 (bf16 pairs), the three terms (bf16 pairs, 32 columns each; two buffers)
+constexpr uint32_t kTmQK = 0, kTmO = 64, kTmS = 128, kTmA = 256, kTmT = 320;
+constexpr int kOutThreads = 17 * 32;
+constexpr int kRing = 8;  // chunks' gate factors
 
-struct __align__(16) Factors {  // (read four at a time)
-    float G[C], f[C], w[C], e[C];  // prefix sums; 2^{R - G}; decay to the chunk's end; scale * decay from its start
-    float2 decay;                  // of the chunk
-    float ref;                     // R; NaN: the chunk's decay spans too much for one reference
+constexpr float kFarDecay = -100.f;  // log2 of a chunk's decay
+
+struct __align__(16) Factors {
+    // per token: prefix sum G; 2^{-G}; decay to the chunk's end; what O is multiplied by
+    float G[C], f[C], w[C], e[C];
+    float2 decay;  // of the chunk
+    int far;       // the chunk's decay is below kFarDecay
 };
+// A barrier that one side may complete again before the other side has looked (terms and P are
+// written up to a chunk ahead, ds and o are waited for two chunks later) is one of a pair,
+// for even and odd chunks.
 struct OutBars {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t qk, ds, o;       // products done
-    uint64_t state, terms, p; // operands ready: S0 in TMEM, V w, P
+    uint64_t full[kStages], fac[kRing];
+    uint64_t qk, ds[2], o[2];                       // products done
+    uint64_t state, terms[2], p[2], ds_read, qk_read;  // S0, V w and P ready; dS and QK read
     uint64_t drain;
 };
 
@@ -149,21 +217,24 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     if (!locate<false>(a, blockIdx.x / a.H, s)) return;
     if (!in_bounds(s.start >= 0 && s.start + s.len <= a.rows && s.n < a.N && h < a.H, a.status)) return;
     const int nch = (int)((s.len + C - 1) / C);
+    constexpr int kIssuer = 16;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&bars.full[i], 1);
+        for (int i = 0; i < kRing; ++i) mbar_init(&bars.fac[i], 32);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.ds[i], 1);
+            mbar_init(&bars.o[i], 1);
+            mbar_init(&bars.terms[i], 128);
+            mbar_init(&bars.p[i], 128);
         }
         mbar_init(&bars.qk, 1);
-        mbar_init(&bars.ds, 1);
-        mbar_init(&bars.o, 1);
         mbar_init(&bars.state, 256);
-        mbar_init(&bars.terms, 128);
-        mbar_init(&bars.p, 128);
+        mbar_init(&bars.ds_read, 256);
+        mbar_init(&bars.qk_read, 128);
         mbar_init(&bars.drain, 1);
         fence_mbar_init();
     }
-    if (warp == 13) {
+    if (warp == kIssuer) {
         tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
@@ -172,7 +243,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tm = tmem_base;
     bool ok = true;
-    int issued = 0;  // (warp 12) chunks whose loads are issued
+    int issued = 0;  // (issuer) chunks whose loads are issued
 
     if (warp < 8) {
         // ------------------------------------------------------------------
@@ -182,7 +253,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int qd = warp & 3, hf = warp >> 2, v = qd * 32 + lane;
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
         const int64_t srow = (int64_t)v * D + 64 * hf;
-        const float *from = s.nseg > 1 ? a.states + (s.ss * a.H + h) * (int64_t)(D * D)
+        const float *from = s.nseg > 1 ? a.states + (s.ss * a.parts * a.H + h) * (int64_t)(D * D)
                                        : (a.h0 ? a.h0 + (s.n * a.H + h) * (int64_t)(D * D) : nullptr);
         float S[64];
         if (from) {
@@ -196,12 +267,12 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             for (int c = 0; c < 64; ++c) S[c] = 0.f;
         }
         auto publish = [&] {  // S0 as bf16 pairs: this thread's 32 columns of the A operand
-            uint32_t w[16];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < 4; ++q) {
+                uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = pack_bf16(S[32 * q + 2 * e], S[32 * q + 2 * e + 1]);
-                tmem_st16u(tm + lane_off + kTmA + 32 * hf + 16 * q, w);
+                for (int e = 0; e < 8; ++e) w[e] = pack_bf16(S[16 * q + 2 * e], S[16 * q + 2 * e + 1]);
+                tmem_st8u(tm + lane_off + kTmA + 32 * hf + 8 * q, w);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -212,14 +283,16 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int64_t c0 = s.pos / C;
         int32_t snap_left = kc > 0 ? kc - (int32_t)(c0 % kc) : 0;
         int64_t snap_idx = kc > 0 ? c0 / kc : 0;
-        const int j4 = lane & 3;
+        // this lane's row of a stmatrix: tokens (0-7 | 8-15) x channels (0-7 | 8-15) of a block
+        const int orow = 32 * hf + (lane & 7) + ((lane >> 4) << 3), opiece = 4 * qd + ((lane >> 3) & 1);
+        const uint32_t obase = smem_u32(sm + kOffO);
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((s.start + (tid >> 4)) * a.H + h) * D + (tid & 15) * 8;
         const int64_t tstride = a.H * D;
-        __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.out) + ((s.start + 32 * hf + j4) * a.H + h) * D + (v - j4);
-        for (int c = 0; c < nch && ok; ++c, op += C * tstride) {
-            const uint32_t par = c & 1;
+        for (int c = 0; c < nch && ok; ++c, out += C * tstride) {
+            const uint32_t par = (c >> 1) & 1;
             const Factors &fac = ring[c % kRing];
-            ok = warp_wait(&bars.terms, par);  // (the factors were written before)
-            ok = ok && warp_wait(&bars.ds, par);
+            ok = warp_wait(&bars.fac[c % kRing], (c / kRing) & 1);
+            ok = ok && warp_wait(&bars.ds[c & 1], par);
             if (!ok) break;
             tc_fence_after();
             const float2 d = fac.decay;
@@ -228,19 +301,50 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 float x[16];
                 tmem_ld16(tm + lane_off + kTmS + 64 * hf + 16 * q, x);
                 tmem_wait_ld();
+                if (d.y != 0.f)  // (a fixed decay, in two floats)
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) x[t] = fmaf(d.y, S[16 * q + t], x[t]);
 #pragma unroll
                 for (int t = 0; t < 16; t += 2) {
-                    const float2 s0 = make_float2(S[16 * q + t], S[16 * q + t + 1]);
-                    const float2 lo = __ffma2_rn(make_float2(d.y, d.y), s0, make_float2(x[t], x[t + 1]));
-                    const float2 r = __ffma2_rn(make_float2(d.x, d.x), s0, lo);
+                    const float2 r = __ffma2_rn(make_float2(d.x, d.x), make_float2(S[16 * q + t], S[16 * q + t + 1]),
+                                                make_float2(x[t], x[t + 1]));
                     S[16 * q + t] = r.x;
                     S[16 * q + t + 1] = r.y;
                 }
             }
-            publish();  // of the next chunk (this chunk's D1 is done: it was issued before dS)
+            tc_fence_before();
+            mbar_arrive(&bars.ds_read);
+            ok = warp_wait(&bars.o[c & 1], par);
+            if (!ok) break;
+            tc_fence_after();
+            // o = scale 2^G O, rounded, turned from channel rows to token rows
+            const uint32_t ob = obase + (c & 1) * 16384;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {  // channels 16 m ..
+                float x[16];
+                tmem_ld_frag32(tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmO + 32 * hf, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int n = 0; n < 4; n += 2) {
+                    const float2 e0 = *reinterpret_cast<const float2 *>(fac.e + 32 * hf + 8 * n + 2 * (lane & 3));
+                    const float2 e1 = *reinterpret_cast<const float2 *>(fac.e + 32 * hf + 8 * n + 8 + 2 * (lane & 3));
+                    const float *y = x + 4 * n;
+                    stsm_x4_trans(ob + (uint32_t)(orow + 8 * n) * 256u + (((uint32_t)(opiece + 2 * m) ^ (uint32_t)(orow & 7)) << 4),
+                                  pack_bf16(y[0] * e0.x, y[1] * e0.y), pack_bf16(y[2] * e0.x, y[3] * e0.y),
+                                  pack_bf16(y[4] * e1.x, y[5] * e1.y), pack_bf16(y[6] * e1.x, y[7] * e1.y));
+                }
+            }
+            publish();  // of the next chunk; O is read too
+            named_bar_sync(1, 256);
+            const int L = (int)(s.len - (int64_t)c * C < C ? s.len - (int64_t)c * C : C);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // a token's 256 bytes by 16 lanes
+                const int t = (tid >> 4) + 16 * i;
+                const uint4 y = ld_shared_v4(ob + (uint32_t)t * 256u + (((uint32_t)(tid & 15) ^ (uint32_t)(t & 7)) << 4));
+                if (t < L) *reinterpret_cast<uint4 *>(out + 16 * i * tstride) = y;
+            }
             if (kc > 0 && --snap_left == 0) {
                 snap_left = kc;
-                // a snapshot is whole chunks from the sequence's start
                 if (snap_idx < a.n_snap) {
                     float *dst = a.snaps + ((s.n * a.n_snap + snap_idx) * a.H + h) * (int64_t)(D * D) + srow;
 #pragma unroll
@@ -248,31 +352,6 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         *reinterpret_cast<float4 *>(dst + cc) = make_float4(S[cc], S[cc + 1], S[cc + 2], S[cc + 3]);
                 }
                 ++snap_idx;
-            }
-            ok = warp_wait(&bars.o, par);
-            if (!ok) break;
-            tc_fence_after();
-            const int L = (int)(s.len - (int64_t)c * C < C ? s.len - (int64_t)c * C : C);
-            const float4 *e4 = reinterpret_cast<const float4 *>(fac.e + 32 * hf);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float x[16], y[16];
-                tmem_ld16(tm + lane_off + kTmD1 + 64 * par + 32 * hf + 16 * q, x);
-                tmem_ld16(tm + lane_off + kTmD2 + 64 * par + 32 * hf + 16 * q, y);
-                tmem_wait_ld();
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const float4 e = e4[4 * q + b];
-                    const float2 r01 = __ffma2_rn(make_float2(x[4 * b], x[4 * b + 1]), make_float2(e.x, e.y),
-                                                  make_float2(y[4 * b], y[4 * b + 1]));
-                    const float2 r23 = __ffma2_rn(make_float2(x[4 * b + 2], x[4 * b + 3]), make_float2(e.z, e.w),
-                                                  make_float2(y[4 * b + 2], y[4 * b + 3]));
-                    // four tokens of this channel -> four channels of one token
-                    uint32_t p01 = pack_bf16(r01.x, r01.y), p23 = pack_bf16(r23.x, r23.y);
-                    quad_transpose(p01, p23, lane);
-                    const int t = 16 * q + 4 * b;
-                    if (32 * hf + t + j4 < L) *reinterpret_cast<uint2 *>(op + t * tstride) = make_uint2(p01, p23);
-                }
             }
         }
         if (ok && a.final_state && s.j == s.nseg - 1) {
@@ -283,11 +362,65 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------------
-        // Gates, V w and P.  P's 64 rows belong to the first two warps (rows 32 w ..), of
-        // which the second has twice the work: the V w tile is dealt out the other way.
+        // The terms of V w: value channels 32 (warp - 8) .. + 31.
         // ------------------------------------------------------------------
-        const int w = warp - 8, t128 = tid - 256;
-        const int part0 = w == 0 ? 0 : (w == 1 ? 8 : (w == 2 ? 12 : 22)), parts = w == 0 ? 8 : (w == 1 ? 4 : 10);
+        const int w = warp - 8;
+        const uint32_t to = tm + ((uint32_t)(w * 32) << 16) + kTmT;
+        for (int c = 0; c < nch && ok; ++c) {
+            const int stage = c % kStages;
+            uint8_t *st = sm + stage * kStage;
+            const Factors &fac = ring[c % kRing];
+            const int L = (int)(s.len - (int64_t)c * C < C ? s.len - (int64_t)c * C : C);
+            ok = warp_wait(&bars.fac[c % kRing], (c / kRing) & 1);
+            ok = ok && warp_wait(&bars.full[stage], (c / kStages) & 1);
+            if (!ok) break;
+            if (L < C) {  // rows behind the sequence: whatever lies there stays out of the sums
+                for (int i = tid - 256; i < 64 * 8; i += 128)
+                    if ((i >> 3) >= L) {
+                        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(st + kStK + i * 16) = z;
+                        *reinterpret_cast<uint4 *>(st + kStK + kHalfQK + i * 16) = z;
+                        *reinterpret_cast<uint4 *>(st + kStV + i * 16) = z;
+                        *reinterpret_cast<uint4 *>(st + kStV + kHalfV + i * 16) = z;
+                    }
+                fence_async_smem();
+                named_bar_sync(2, 128);
+            }
+            if (c > 1) ok = warp_wait(&bars.ds[c & 1], ((c >> 1) & 1) ^ 1);  // dS of chunk c - 2 has read this buffer
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t from = terms_address(smem_u32(st + kStV) + (uint32_t)(w >> 1) * kHalfV, 0, 0, lane);
+            const int piece = (w & 1) * 4;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {  // 16 channels x 16 tokens each
+                const int m = i >> 2, n = i & 3;
+                uint32_t t0[4], t1[4], t2[4];
+                // (the piece's bits are turned by the row's: exclusive or)
+                channel_terms((from ^ (uint32_t)((piece + 2 * m) << 4)) + n * 2048u, fac.w + 16 * n, lane, t0, t1, t2);
+                const uint32_t at = to + (c & 1) * 96 + ((uint32_t)(16 * m) << 16) + 8 * n;
+                tmem_st_frag8(at, t0);
+                tmem_st_frag8(at + 32, t1);
+                tmem_st_frag8(at + 64, t2);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars.terms[c & 1]);
+        }
+    } else if (warp < kIssuer) {
+        // ------------------------------------------------------------------
+        // P: query tokens 16 w .. 16 w + 15, of which a lane holds two (i0, i0 + 8).  Warp 12
+        // forms the gates' factors, two chunks ahead (two tokens per lane).
+        // ------------------------------------------------------------------
+        const int w = warp - 12, i0 = 16 * w + (lane >> 2), j0 = 2 * (lane & 3);
+        uint8_t *P = sm + kOffP;
+        // this lane's row of a stmatrix: matrices (tokens 0-7, keys 0-7), (8-15, 0-7), (0-7, 8-15),
+        // (8-15, 8-15) of a block
+        const int prow = 16 * w + (lane & 15);
+        const uint32_t paddr = smem_u32(P) + (uint32_t)prow * 128u + (((uint32_t)(lane >> 4) ^ (uint32_t)(prow & 7)) << 4);
+        for (int i = lane; i < 2 * 16 * 8; i += 32)  // the blocks above the diagonal stay zero
+            *reinterpret_cast<uint4 *>(P + (i >> 7) * 8192 + (16 * w + ((i >> 3) & 15)) * 128 + (i & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
         const float gh = fixed ? a.g[h] * kLog2e : 0.f;
         auto load_gate = [&](int c) {
             const int64_t t = (int64_t)c * C + 2 * lane;
@@ -301,206 +434,164 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             g = load_gate(0);
             if (fixed) fixed_decay = exp2_pair((double)a.g[h] * 1.4426950408889634074 * C);
         }
-        uint8_t *T = sm + kOffT, *P = sm + kOffP;
-        // the blocks above the diagonal stay zero
-        if (w == 0)
-            for (int j = 4; j < 8; ++j)
-                *reinterpret_cast<uint4 *>(P + sw128_offset(lane, j)) = make_uint4(0u, 0u, 0u, 0u);
-        for (int c = 0; c < nch && ok; ++c) {
-            const int stage = c % kStages;
-            const uint32_t par = c & 1;
-            uint8_t *st = sm + stage * kStage;
-            Factors &fac = ring[c % kRing];
-            const int L = (int)(s.len - (int64_t)c * C < C ? s.len - (int64_t)c * C : C);
-            if (w == 0) {
+        for (int c = -2; c < nch && ok; ++c) {
+            if (w == 0 && c + 2 < nch) {
+                // The slot's last readers, of chunk c - 6, are done: O of chunk c - 3 was formed
+                // (this warp waited for it), after O of chunk c - 4 was read.
+                const int cf = c + 2;
+                Factors &fac = ring[cf % kRing];
                 float2 G, after;
                 float total;
                 scan_gates(g.x, g.y, lane, G, after, total);
-                // One reference R in the middle keeps both factors of 2^{G_i - G_j} inside 2^+-60.
-                const float ref = total > -120.f ? 0.5f * total : __int_as_float(0x7fc00000);
+                const bool far = !(total > kFarDecay);
                 *reinterpret_cast<float2 *>(&fac.G[2 * lane]) = G;
-                *reinterpret_cast<float2 *>(&fac.f[2 * lane]) = make_float2(ex2(ref - G.x), ex2(ref - G.y));
+                *reinterpret_cast<float2 *>(&fac.f[2 * lane]) = make_float2(ex2(-G.x), ex2(-G.y));
                 *reinterpret_cast<float2 *>(&fac.w[2 * lane]) = make_float2(ex2(after.x), ex2(after.y));
-                *reinterpret_cast<float2 *>(&fac.e[2 * lane]) = make_float2(a.scale * ex2(G.x), a.scale * ex2(G.y));
+                *reinterpret_cast<float2 *>(&fac.e[2 * lane]) =
+                    far ? make_float2(1.f, 1.f) : make_float2(a.scale * ex2(G.x), a.scale * ex2(G.y));
                 if (lane == 0) {
-                    fac.ref = ref;
+                    const int64_t left = s.len - (int64_t)cf * C;
+                    fac.far = far;
                     fac.decay = !fixed ? make_float2(ex2(total), 0.f)
-                                       : (L == C ? fixed_decay : exp2_pair((double)a.g[h] * 1.4426950408889634074 * L));
+                                       : (left >= C ? fixed_decay
+                                                    : exp2_pair((double)a.g[h] * 1.4426950408889634074 * (double)left));
                 }
-                if (c + 1 < nch) g = load_gate(c + 1);
+                mbar_arrive(&bars.fac[cf % kRing]);
+                if (cf + 1 < nch) g = load_gate(cf + 1);
             }
-            named_bar_sync(1, 128);
-            ok = warp_wait(&bars.full[stage], (c / kStages) & 1);
-            // the terms' buffer: the previous chunk's dS has read it
-            if (c > 0) ok = ok && warp_wait(&bars.ds, par ^ 1);
-            if (!ok) break;
-            if (L < C) {  // rows behind the sequence: whatever lies there stays out of the sums
-                for (int i = t128; i < 64 * 8; i += 128) {
-                    const uint32_t at = (uint32_t)i * 16;
-                    if ((i >> 3) >= L) {
-                        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(st + kStK + at) = z;
-                        *reinterpret_cast<uint4 *>(st + kStK + kHalfQK + at) = z;
-                        *reinterpret_cast<uint4 *>(st + kStV + at) = z;
-                        *reinterpret_cast<uint4 *>(st + kStV + kHalfV + at) = z;
-                    }
-                }
-            }
-#pragma unroll 2
-            for (int i = 0; i < parts; ++i) {
-                const uint32_t at = (uint32_t)((part0 + i) * 32 + lane) * 16;  // 16-byte piece of the V tile
-                const int row = (at >> 7) & 63;
-                uint4 t[3];
-                if (row < L) {
-                    split_terms(*reinterpret_cast<const uint4 *>(st + kStV + at), fac.w[row], t);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) t[k] = make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(T + k * 16384 + at) = t[k];
-            }
-            fence_async_smem();
-            mbar_arrive(&bars.terms);
-            if (c > 0) ok = warp_wait(&bars.o, par ^ 1);  // P's buffer: the previous chunk's D2 has read it
-            ok = ok && warp_wait(&bars.qk, par);
+            if (c < 0) continue;
+            const Factors &fac = ring[c % kRing];
+            ok = warp_wait(&bars.fac[c % kRing], (c / kRing) & 1);
+            ok = ok && warp_wait(&bars.qk, c & 1);
+            if (c > 1) ok = ok && warp_wait(&bars.o[c & 1], ((c >> 1) & 1) ^ 1);  // O of chunk c - 2 has read this buffer
             if (!ok) break;
             tc_fence_after();
-            if (w < 2) {
-                const int i = 32 * w + lane;
-                const float ref = fac.ref, Gi = fac.G[i];
-                const bool one_ref = ref == ref;
-                const float ei = a.scale * ex2(one_ref ? Gi - ref : 0.f);
+            const bool far = fac.far;
+#pragma unroll 1
+            for (int n = 0; n <= w; ++n) {  // 16 keys each
+                float x[8];
+                tmem_ld_frag16(tm + ((uint32_t)(w * 32) << 16) + kTmQK + 16 * n, x);
+                tmem_wait_ld();
+                float2 f[4];  // factors of keys j, j + 1 and j + 8, j + 9: for token i0, then for i0 + 8
+                if (!far) {
+                    f[0] = f[1] = *reinterpret_cast<const float2 *>(fac.f + 16 * n + j0);
+                    f[2] = f[3] = *reinterpret_cast<const float2 *>(fac.f + 16 * n + 8 + j0);
+                } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q > 2 * w + 1) break;
-                    float x[16];
-                    tmem_ld16(tm + ((uint32_t)(w * 32) << 16) + kTmQK + 16 * q, x);
-                    tmem_wait_ld();
-                    uint32_t o[8];
-                    if (one_ref) {
-                        const float4 *f4 = reinterpret_cast<const float4 *>(fac.f + 16 * q);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const float4 f = f4[b];
-                            const float ff[4] = {f.x, f.y, f.z, f.w};
-                            float y[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) y[e] = 16 * q + 4 * b + e <= i ? (x[4 * b + e] * ei) * ff[e] : 0.f;
-                            o[2 * b] = pack_bf16(y[0], y[1]);
-                            o[2 * b + 1] = pack_bf16(y[2], y[3]);
-                        }
-                    } else {
-                        const float4 *G4 = reinterpret_cast<const float4 *>(fac.G + 16 * q);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const float4 G = G4[b];
-                            const float gg[4] = {G.x, G.y, G.z, G.w};
-                            float y[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                y[e] = 16 * q + 4 * b + e <= i ? x[4 * b + e] * (ei * ex2(Gi - gg[e])) : 0.f;
-                            o[2 * b] = pack_bf16(y[0], y[1]);
-                            o[2 * b + 1] = pack_bf16(y[2], y[3]);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float Gi = fac.G[i0 + 8 * (e & 1)];
+                        const float2 Gj = *reinterpret_cast<const float2 *>(fac.G + 16 * n + 8 * (e >> 1) + j0);
+                        f[e] = make_float2(a.scale * ex2(Gi - Gj.x), a.scale * ex2(Gi - Gj.y));
                     }
-                    *reinterpret_cast<uint4 *>(P + sw128_offset(i, 2 * q)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(P + sw128_offset(i, 2 * q + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 p = __fmul2_rn(make_float2(x[2 * e], x[2 * e + 1]), f[e]);
+                    const int i = i0 + 8 * (e & 1), j = 16 * n + 8 * (e >> 1) + j0;
+                    if (j > i) p.x = 0.f;
+                    if (j + 1 > i) p.y = 0.f;
+                    o[e] = pack_bf16(p.x, p.y);
+                }
+                stsm_x4((paddr ^ (uint32_t)(n << 5)) + (c & 1) * 8192, o[0], o[1], o[2], o[3]);
             }
             tc_fence_before();
+            mbar_arrive(&bars.qk_read);
+            if (far) {  // Q by scale 2^G, in place (QK is done with it)
+                uint8_t *Q = sm + (c % kStages) * kStage + kStQ;
+                for (int i = lane; i < 16 * 16; i += 32) {
+                    const int row = 16 * w + (i >> 4);
+                    uint4 *q = reinterpret_cast<uint4 *>(Q + ((i >> 3) & 1) * kHalfQK + row * 128 + (i & 7) * 16);
+                    const float f = a.scale * ex2(fac.G[row]);
+                    uint4 t = *q;
+                    uint32_t *u = &t.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = pack_bf16(f * __uint_as_float(u[e] << 16), f * __uint_as_float(u[e] & 0xffff0000u));
+                    *q = t;
+                }
+            }
             fence_async_smem();
-            mbar_arrive(&bars.p);
+            mbar_arrive(&bars.p[c & 1]);
         }
-    } else if (warp == 12) {
+    } else {
         // ------------------------------------------------------------------
-        // Loads
+        // Loads and MMAs
         // ------------------------------------------------------------------
-        if (lane == 0) {
-            prefetch_tmap(&mq);
-            prefetch_tmap(&mk);
-            prefetch_tmap(&mv);
-            const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
-            for (int c = 0; c < nch; ++c) {
-                const int stage = c % kStages;
-                if (c >= kStages && !(ok = mbar_wait(&bars.empty[stage], ((c / kStages) & 1) ^ 1))) break;
-                uint8_t *st = sm + stage * kStage;
-                uint64_t *bar = &bars.full[stage];
+        const uint32_t base = smem_u32(sm);
+        const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
+        auto load = [&](int c) {
+            if (lane == 0) {
+                uint8_t *st = sm + (c % kStages) * kStage;
+                uint64_t *bar = &bars.full[c % kStages];
                 const int32_t row = (int32_t)(s.start + (int64_t)c * C);
                 mbar_arrive_expect_tx(bar, kStage);
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     tma_load_3d(st + kStQ + i * kHalfQK, &mq, 64 * i, hq, row, bar);
                     tma_load_3d(st + kStK + i * kHalfQK, &mk, 64 * i, hq, row, bar);
                     tma_load_3d(st + kStV + i * kHalfV, &mv, 64 * i, hv, row, bar);
                 }
-                issued = c + 1;
             }
-        }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-    } else {
-        // ------------------------------------------------------------------
-        // MMAs
-        // ------------------------------------------------------------------
-        const uint32_t base = smem_u32(sm);
+            issued = c + 1;
+            __syncwarp();
+        };
         auto issue_qk = [&](int c) {
             const uint32_t st = base + (c % kStages) * kStage;
             const uint64_t aq = sdesc_sw128(st + kStQ, 16, 1024), bk = sdesc_sw128(st + kStK, 16, 1024);
-#pragma unroll
+#pragma unroll 4
             for (int kk = 0; kk < 8; ++kk) {
                 const uint64_t at = (uint64_t)(((kk >> 2) * kHalfQK + (kk & 3) * 32) >> 4);
-                mma_bf16_ss(tm + kTmQK, aq + at, bk + at, idesc_bf16(128, 64, 0, 0), kk > 0);
+                mma_bf16_ss(tm + kTmQK, aq + at, bk + at, idesc_bf16(64, 64, 0, 0), kk > 0);
             }
             mma_commit_warp(&bars.qk);
         };
-        if (nch > 0) {
-            ok = warp_wait(&bars.full[0], 0);
-            if (ok) issue_qk(0);
+        if (lane == 0) {
+            prefetch_tmap(&mq);
+            prefetch_tmap(&mk);
+            prefetch_tmap(&mv);
         }
-        for (int c = 0; c < nch && ok; ++c) {
-            const int stage = c % kStages;
-            const uint32_t par = c & 1, st = base + stage * kStage;
-            ok = warp_wait(&bars.state, par);
-            if (!ok) break;
-            tc_fence_after();
-            {  // D1 (its buffer and dS's are free: the state of chunk c was published after their last reads)
-                const uint64_t bq = sdesc_sw128(st + kStQ, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ts(tm + kTmD1 + 64 * par, tm + kTmA + kk * 8,
-                                bq + (uint64_t)(((kk >> 2) * kHalfQK + (kk & 3) * 32) >> 4), idesc_bf16(128, 64, 0, 0),
-                                kk > 0);
-            }
-            ok = warp_wait(&bars.terms, par);
-            if (!ok) break;
-            tc_fence_after();
-            {  // dS
+        for (int c = 0; c < 2 && c < nch; ++c) load(c);
+        for (int c = -1; c < nch && ok; ++c) {
+            const uint32_t par = c & 1, st = base + (c % kStages) * kStage;
+            if (c >= 0) {  // dS
+                if (c > 0) ok = warp_wait(&bars.ds_read, par ^ 1);
+                ok = ok && warp_wait(&bars.terms[par], (c >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
                 const uint64_t bk = sdesc_sw128(st + kStK, kHalfQK, 1024);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const uint64_t at = sdesc_sw128(base + kOffT + k * 16384, kHalfV, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ss(tm + kTmS, at + (uint64_t)((kk * 2048) >> 4), bk + (uint64_t)((kk * 2048) >> 4),
-                                    idesc_bf16(128, 128, 1, 1), k > 0 || kk > 0);
-                }
-                mma_commit_warp(&bars.ds);
-            }
-            ok = warp_wait(&bars.p, par);
-            if (!ok) break;
-            tc_fence_after();
-            {  // D2
-                const uint64_t av = sdesc_sw128(st + kStV, kHalfV, 1024), bp = sdesc_sw128(base + kOffP, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ss(tm + kTmD2 + 64 * par, av + (uint64_t)((kk * 2048) >> 4), bp + (uint64_t)((kk * 32) >> 4),
-                                idesc_bf16(128, 64, 1, 0), kk > 0);
-                mma_commit_warp(&bars.o);
-                mma_commit_warp(&bars.empty[stage]);
+                const uint32_t t = tm + kTmT + 96 * par;
+#pragma unroll 4
+                for (int i = 0; i < 12; ++i)
+                    mma_bf16_ts(tm + kTmS, t + 8 * i, bk + (uint64_t)(((i & 3) * 2048) >> 4), idesc_bf16(128, 128, 0, 1),
+                                i > 0);
+                mma_commit_warp(&bars.ds[par]);
             }
             if (c + 1 < nch) {
                 ok = warp_wait(&bars.full[(c + 1) % kStages], ((c + 1) / kStages) & 1);
-                if (ok) issue_qk(c + 1);
+                if (c >= 0) ok = ok && warp_wait(&bars.qk_read, par);
+                if (!ok) break;
+                tc_fence_after();
+                issue_qk(c + 1);
+            }
+            if (c >= 0) {  // O
+                ok = warp_wait(&bars.state, par);  // S0 in place, the previous chunk's O read
+                if (!ok) break;
+                if (c + 2 < nch) load(c + 2);  // into the previous chunk's stage: all its products are done
+                ok = warp_wait(&bars.p[par], (c >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t bq = sdesc_sw128(st + kStQ, 16, 1024);
+                const uint64_t av = sdesc_sw128(st + kStV, kHalfV, 1024), bp = sdesc_sw128(base + kOffP + par * 8192, 16, 1024);
+#pragma unroll 4
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16_ts(tm + kTmO, tm + kTmA + kk * 8, bq + (uint64_t)(((kk >> 2) * kHalfQK + (kk & 3) * 32) >> 4),
+                                idesc_bf16(128, 64, 0, 0), kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16_ss(tm + kTmO, av + (uint64_t)((kk * 2048) >> 4), bp + (uint64_t)((kk * 32) >> 4),
+                                idesc_bf16(128, 64, 1, 0), 1);
+                mma_commit_warp(&bars.o[par]);
             }
         }
     }
@@ -509,134 +600,174 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         // A wait gave up: record it.  Every other role's next wait gives up too (it waits,
         // directly or not, for this one), so all of them get here.
         if (lane == 0) flag_error(a.status, GDN_DEV_TIMEOUT_SCAN);
-        if (warp == 12 && lane == 0)
+        if (warp == kIssuer) {  // loads and MMAs still in flight
             for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
-                mbar_wait(&bars.full[j % kStages], (j / kStages) & 1);
-        if (warp == 13) {
+                warp_wait(&bars.full[j % kStages], (j / kStages) & 1);
             mma_commit_warp(&bars.drain);
             warp_wait(&bars.drain, 0);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 13) tmem_dealloc(tm, 512);
+    if (warp == kIssuer) tmem_dealloc(tm, 512);
 }
 
 // ===========================================================================
-// State kernel: U of a segment (not its sequence's last) and its decay
+// State kernel: what a part of a segment (not its sequence's last) adds to the state
+// at the segment's end
 // ===========================================================================
-// Backwards from the segment's end, so that a token's weight is the sum of the gates after
-// it and the products add up in TMEM without a rescale; it stops where nothing earlier
-// reaches the end.  Warps 0-7: gates and V w (two buffers); warp 8: loads and MMAs.
+// Backwards from the part's end, so that a token's weight is the sum of the gates after it
+// and the products add up in TMEM without a rescale; it stops where nothing earlier
+// reaches the segment's end.  A segment is cut into parts so that the heads whose
+// state lasts do not hold up the rest: their parts run side by side, and a part
+// behind which the decay has left nothing ends at once.
+// Warps 0-7: the terms of V w (32 value channels and 32 tokens a warp);
+// warp 8: loads and MMAs.  Two blocks per SM (98 KB, 256 TMEM columns each).
 constexpr uint32_t kSsK = 0, kSsV = 16384, kSsStage = 32768;
 constexpr int kSsStages = 3;
-constexpr uint32_t kSsOffT = kSsStages * kSsStage, kSsTerms = 3 * 16384;
-constexpr uint32_t kStateSmem = kSsOffT + 2 * kSsTerms + 1024;
+constexpr uint32_t kStateSmem = kSsStages * kSsStage + 1024;
+constexpr uint32_t kTmU = 0, kTmUT = 128;
 constexpr int kStateThreads = 9 * 32;
 
 struct StateBars {
-    uint64_t full[kSsStages], terms[2], ds[2], drain;
+    uint64_t full[kSsStages], terms, ds, drain;
 };
 
-__global__ void __launch_bounds__(kStateThreads, 1)
+__global__ void __launch_bounds__(kStateThreads, 2)
 gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Args a,
                      const bool fixed) {
     extern __shared__ unsigned char smem_raw[];
     uint8_t *sm = align1024(smem_raw);
     __shared__ StateBars bars;
     __shared__ uint32_t tmem_base;
-    __shared__ int s_last;  // index of the last chunk to add, once known
+    __shared__ int s_last;                     // index of the last chunk to add, once known
+    __shared__ __align__(16) float s_w[8][C];  // the chunk's weights, a copy per warp
+    __shared__ float s_sum[8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t h = blockIdx.x % a.H;
+    const int64_t h = blockIdx.x % a.H, unit = blockIdx.x / a.H;
+    const int64_t part = unit % a.parts;
     Slot s;
-    if (!locate<true>(a, blockIdx.x / a.H, s) || s.nseg < 2 || s.j == s.nseg - 1) return;
+    if (!locate<true>(a, unit / a.parts, s) || s.nseg < 2 || s.j == s.nseg - 1) return;
     if (!in_bounds(s.start >= 0 && s.start + s.len <= a.rows && s.n < a.N && s.ss < a.sslots && s.len % C == 0, a.status))
         return;
-    const int nch = (int)(s.len / C);
+    const int64_t begin = part * a.part_len;  // of the part, in the segment
+    const int64_t end = begin + a.part_len < s.len ? begin + a.part_len : s.len;
+    const int nch = (int)((end - begin) / C);
+    // the decay from the part's end to the segment's
+    const double g64 = fixed ? (double)a.g[h] * 1.4426950408889634074 : 0.0;
+    float gap = fixed ? (float)(g64 * (double)(s.len - end)) : 0.f;
+    if (!fixed) {
+        constexpr int kSpan = 2048;
+        for (int64_t t1 = s.len; t1 > end && gap > kDead; t1 -= kSpan) {
+            float sum = 0.f;
+            if (warp < 8)
+                for (int64_t t = t1 - 1 - tid; t >= end && t >= t1 - kSpan; t -= 256) sum += a.g[(s.start + t) * a.H + h];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            __syncthreads();
+            if (warp < 8 && lane == 0) s_sum[warp] = sum;
+            __syncthreads();
+            float all = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) all += s_sum[w];
+            gap += all * kLog2e;
+        }
+    }
+    const int64_t at = (s.ss * a.parts + part) * a.H + h;
+    const bool alive = nch > 0 && gap > kDead;
+    if (tid == 0) {
+        a.alive[at] = alive ? 1 : 0;
+        if (part == 0 && !alive) a.tot[s.ss * a.H + h] = (double)gap;
+    }
+    if (!alive) return;
     if (tid == 0) {
         for (int i = 0; i < kSsStages; ++i) mbar_init(&bars.full[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.terms[i], 256);
-            mbar_init(&bars.ds[i], 1);
-        }
+        mbar_init(&bars.terms, 256);
+        mbar_init(&bars.ds, 1);
         mbar_init(&bars.drain, 1);
         s_last = nch - 1;
         fence_mbar_init();
     }
     if (warp == 8) {
-        tmem_alloc(&tmem_base, 128);
+        tmem_alloc(&tmem_base, 256);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base;
+    const int64_t row_end = s.start + end;
     bool ok = true;
     int issued = 0, waited = 0;  // (warp 8) loads
     if (warp < 8) {
         const float gh = fixed ? a.g[h] * kLog2e : 0.f;
-        auto load_gate = [&](int i) {  // chunk i from the segment's end
+        auto load_gate = [&](int i) {  // chunk i from the part's end
             if (fixed) return make_float2(gh, gh);
-            const float *p = a.g + (s.start + (int64_t)(nch - 1 - i) * C + 2 * lane) * a.H + h;
+            const float *p = a.g + (row_end - (int64_t)(i + 1) * C + 2 * lane) * a.H + h;
             return make_float2(p[0] * kLog2e, p[a.H] * kLog2e);
         };
+        const int qd = warp & 3, hf = warp >> 2, v = qd * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+        float *wts = s_w[warp];
         float2 g = load_gate(0);
-        float after_chunk = 0.f;
-        const int row = tid >> 3;  // the V rows of this thread: row and row + 32
+        float after_chunk = gap;
         int i = 0;
         for (; i < nch; ++i) {
-            const int stage = i % kSsStages, buf = i & 1;
-            const uint8_t *V = sm + stage * kSsStage + kSsV;
-            uint8_t *T = sm + kSsOffT + buf * kSsTerms;
+            const int stage = i % kSsStages;
             float2 G, after;
             float total;
             scan_gates(g.x, g.y, lane, G, after, total);
-            const float w0 = ex2(after.x + after_chunk), w1 = ex2(after.y + after_chunk);
-            float wr[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int r = row + 32 * k;
-                const float x = __shfl_sync(0xffffffffu, w0, r >> 1), y = __shfl_sync(0xffffffffu, w1, r >> 1);
-                wr[k] = r & 1 ? y : x;
-            }
+            __syncwarp();
+            *reinterpret_cast<float2 *>(wts + 2 * lane) = make_float2(ex2(after.x + after_chunk), ex2(after.y + after_chunk));
+            __syncwarp();
             after_chunk += total;
             const bool last = i == nch - 1 || after_chunk <= kDead;  // (the same in every warp)
             if (!last) g = load_gate(i + 1);
             ok = warp_wait(&bars.full[stage], (i / kSsStages) & 1);
-            if (i >= 2) ok = ok && warp_wait(&bars.ds[buf], ((i >> 1) & 1) ^ 1);
             if (!ok) break;
+            uint32_t t0[2][2][4], t1[2][2][4], t2[2][2][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t at = (uint32_t)(tid + 256 * k) * 16;
-                uint4 t[3];
-                split_terms(*reinterpret_cast<const uint4 *>(V + at), wr[k & 1], t);
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4 *>(T + m * 16384 + at) = t[m];
-            }
+                for (int n = 0; n < 2; ++n)
+                    channel_terms(terms_address(smem_u32(sm + stage * kSsStage + kSsV) + (uint32_t)(qd >> 1) * 8192u,
+                                                (qd & 1) * 4 + 2 * m, 32 * hf + 16 * n, lane),
+                                  wts + 32 * hf + 16 * n, lane, t0[m][n], t1[m][n], t2[m][n]);
+            if (i > 0) ok = warp_wait(&bars.ds, (i & 1) ^ 1);  // the previous chunk's products have read the terms
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const uint32_t to = tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmUT + 16 * hf + 8 * n;
+                    tmem_st_frag8(to, t0[m][n]);
+                    tmem_st_frag8(to + 32, t1[m][n]);
+                    tmem_st_frag8(to + 64, t2[m][n]);
+                }
+            tmem_wait_st();
             if (last && tid == 0) s_last = i;
-            fence_async_smem();
-            mbar_arrive(&bars.terms[buf]);
+            tc_fence_before();
+            mbar_arrive(&bars.terms);
             if (last) break;
         }
         if (ok) {
-            ok = warp_wait(&bars.ds[i & 1], (i >> 1) & 1);  // the last chunk's products, and all before
+            ok = warp_wait(&bars.ds, i & 1);  // the last chunk's products, and all before
             tc_fence_after();
         }
         if (ok) {
-            const int qd = warp & 3, hf = warp >> 2, v = qd * 32 + lane;
-            float *U = a.states + (s.ss * a.H + h) * (int64_t)(D * D) + (int64_t)v * D + 64 * hf;
+            float *U = a.states + at * (int64_t)(D * D) + (int64_t)v * D + 64 * hf;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float x[16];
-                tmem_ld16(tm + ((uint32_t)(qd * 32) << 16) + 64 * hf + 16 * q, x);
+                tmem_ld16(tm + lane_off + kTmU + 64 * hf + 16 * q, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int t = 0; t < 16; t += 4)
-                    *reinterpret_cast<float4 *>(U + 16 * q + t) = make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
+                for (int e = 0; e < 16; e += 4)
+                    *reinterpret_cast<float4 *>(U + 16 * q + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
             }
             // the segment's decay (once it is past kDead, how far past does not matter)
-            if (tid == 0)
-                a.tot[s.ss * a.H + h] = fixed ? (double)a.g[h] * 1.4426950408889634074 * (double)s.len : (double)after_chunk;
+            if (part == 0 && tid == 0) a.tot[s.ss * a.H + h] = fixed ? g64 * (double)s.len : (double)after_chunk;
         }
     } else {
         const uint32_t base = smem_u32(sm);
@@ -646,7 +777,7 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
             if (lane == 0) {
                 uint8_t *st = sm + stage * kSsStage;
                 uint64_t *bar = &bars.full[stage];
-                const int32_t r = (int32_t)(s.start + (int64_t)(nch - 1 - i) * C);
+                const int32_t r = (int32_t)(row_end - (int64_t)(i + 1) * C);
                 mbar_arrive_expect_tx(bar, kSsStage);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -655,32 +786,28 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
                 }
             }
             issued = i + 1;
+            __syncwarp();
         };
         for (int i = 0; i < 2 && i < nch; ++i) load(i);
         for (int i = 0; i < nch; ++i) {
-            const int stage = i % kSsStages, buf = i & 1;
+            const int stage = i % kSsStages;
             ok = warp_wait(&bars.full[stage], (i / kSsStages) & 1);
             if (!ok) break;
             waited = i + 1;
-            ok = warp_wait(&bars.terms[buf], (i >> 1) & 1);
+            ok = warp_wait(&bars.terms, i & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t bk = sdesc_sw128(base + stage * kSsStage + kSsK, 8192, 1024);
 #pragma unroll
-            for (int m = 0; m < 3; ++m) {
-                const uint64_t at = sdesc_sw128(base + kSsOffT + buf * kSsTerms + m * 16384, 8192, 1024);
+            for (int m = 0; m < 3; ++m)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ss(tm, at + (uint64_t)((kk * 2048) >> 4), bk + (uint64_t)((kk * 2048) >> 4),
-                                idesc_bf16(128, 128, 1, 1), i > 0 || m > 0 || kk > 0);
-            }
-            mma_commit_warp(&bars.ds[buf]);
+                    mma_bf16_ts(tm + kTmU, tm + kTmUT + 32 * m + 8 * kk, bk + (uint64_t)((kk * 2048) >> 4),
+                                idesc_bf16(128, 128, 0, 1), i > 0 || m > 0 || kk > 0);
+            mma_commit_warp(&bars.ds);
             if (*(volatile int *)&s_last == i) break;
-            if (i + 2 < nch) {  // into the stage of chunk i - 1
-                if (i >= 1) ok = warp_wait(&bars.ds[buf ^ 1], ((i - 1) >> 1) & 1);
-                if (!ok) break;
-                load(i + 2);
-            }
+            // into the stage of chunk i - 1, whose products were done before these terms were stored
+            if (i + 2 < nch) load(i + 2);
         }
     }
     __syncwarp();
@@ -695,7 +822,7 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
         for (int j = waited; j < issued; ++j) warp_wait(&bars.full[j % kSsStages], (j / kSsStages) & 1);
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tm, 128);
+    if (warp == 8) tmem_dealloc(tm, 256);
 }
 
 // ===========================================================================
@@ -731,7 +858,7 @@ gdn_status make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t H) {
 }  // namespace
 
 gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s) {
-    const int64_t grid = p.slots * p.H, sgrid = p.sslots * p.H;
+    const int64_t grid = p.slots * p.H, sgrid = p.sslots * p.parts * p.H;
     if (grid > 0x7fffffffLL || sgrid > 0x7fffffffLL) return fail(GDN_ERR_UNSUPPORTED, "grid too large");
     CUtensorMap mq, mk, mv;
     memset(&mq, 0, sizeof mq);
