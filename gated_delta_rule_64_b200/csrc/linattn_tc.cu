@@ -20,14 +20,14 @@
 //
 // The roles run ahead of one another, joined by mbarriers:
 //   warps 0-7    hold the state (two threads per row, 64 columns each): S = 2^G S0 + dS, its
-//                bf16 copy as the A operand of S0 Q^T in TMEM, and the outputs
+//                bf16 copy as the A operand of S0 Q^T in TMEM; they turn O into token rows
 //   warps 8-11   the three terms of V w, 32 value channels a warp, as the A operand of dS in
 //                TMEM (two buffers): transposed on the way from shared memory (ldmatrix)
 //                into the fragment layout that a 16-lane TMEM store takes
-//   warps 12-14  P, 16 query tokens a warp (a 64-row product leaves 16 rows in each TMEM
-//   and 15       quarter), through the fragment layout too: TMEM to stmatrix; warp 12, whose
-//                tokens have the fewest keys, also forms the factors that come from the gates
-//   warp 16      issues the TMA loads (three stages of 48 KB) and the MMAs
+//   warps 12-15  P, 16 query tokens a warp (a 64-row product leaves 16 rows in each TMEM
+//                quarter), through the fragment layout too: TMEM to stmatrix
+//   warp 16      issues the MMAs          warp 17  issues the TMA loads (three stages of 48 KB)
+//   warp 18      stores the outputs       warp 19  the factors that come from the gates
 // One block per SM: 205 KB of shared memory, all 512 TMEM columns.
 //
 // The loops of the roles are kept short on purpose: every scheduler runs a warp of each, and
@@ -178,11 +178,11 @@ __device__ __forceinline__ uint32_t terms_address(uint32_t half, int piece, int 
 constexpr uint32_t kStQ = 0, kStK = 8192, kStV = 32768, kHalfQK = 16384, kHalfV = 8192, kStage = 49152;
 constexpr int kStages = 3;
 constexpr uint32_t kOffP = kStages * kStage;   // P, 64 rows of 128 bytes; two buffers
-constexpr uint32_t kOffO = kOffP + 2 * 8192;   // outputs, 64 rows of 256 bytes (16-byte pieces turned by row); two buffers
+constexpr uint32_t kOffO = kOffP + 2 * 8192;   // outputs, two halves of 64 rows of 128 bytes; two buffers
 constexpr uint32_t kOutSmem = kOffO + 2 * 16384 + 1024;
 // TMEM columns: QK, O, dS, S0 (bf16 pairs), the three terms (bf16 pairs, 32 columns each; two buffers)
 constexpr uint32_t kTmQK = 0, kTmO = 64, kTmS = 128, kTmA = 256, kTmT = 320;
-constexpr int kOutThreads = 17 * 32;
+constexpr int kOutThreads = 20 * 32;
 constexpr int kRing = 8;  // chunks' gate factors
 
 constexpr float kFarDecay = -100.f;  // log2 of a chunk's decay
@@ -197,7 +197,8 @@ struct __align__(16) Factors {
 // written up to a chunk ahead, ds and o are waited for two chunks later) is one of a pair,
 // for even and odd chunks.
 struct OutBars {
-    uint64_t full[kStages], fac[kRing];
+    uint64_t full[kStages], empty[kStages], fac[kRing];
+    uint64_t out_full[2], out_empty[2];
     uint64_t qk, ds[2], o[2];                       // products done
     uint64_t state, terms[2], p[2], ds_read, qk_read;  // S0, V w and P ready; dS and QK read
     uint64_t drain;
@@ -205,7 +206,8 @@ struct OutBars {
 
 __global__ void __launch_bounds__(kOutThreads, 1)
 gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-               const __grid_constant__ CUtensorMap mv, const Args a, const bool fixed) {
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Args a,
+               const bool fixed) {
     extern __shared__ unsigned char smem_raw[];
     uint8_t *sm = align1024(smem_raw);
     __shared__ OutBars bars;
@@ -217,15 +219,20 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     if (!locate<false>(a, blockIdx.x / a.H, s)) return;
     if (!in_bounds(s.start >= 0 && s.start + s.len <= a.rows && s.n < a.N && h < a.H, a.status)) return;
     const int nch = (int)((s.len + C - 1) / C);
-    constexpr int kIssuer = 16;
+    constexpr int kIssuer = 16, kLoader = 17, kStorer = 18;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&bars.full[i], 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
         for (int i = 0; i < kRing; ++i) mbar_init(&bars.fac[i], 32);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.ds[i], 1);
             mbar_init(&bars.o[i], 1);
             mbar_init(&bars.terms[i], 128);
             mbar_init(&bars.p[i], 128);
+            mbar_init(&bars.out_full[i], 256);
+            mbar_init(&bars.out_empty[i], 1);
         }
         mbar_init(&bars.qk, 1);
         mbar_init(&bars.state, 256);
@@ -243,7 +250,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tm = tmem_base;
     bool ok = true;
-    int issued = 0;  // (issuer) chunks whose loads are issued
+    int issued = 0;  // (loader) chunks whose loads are issued
 
     if (warp < 8) {
         // ------------------------------------------------------------------
@@ -284,11 +291,9 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         int32_t snap_left = kc > 0 ? kc - (int32_t)(c0 % kc) : 0;
         int64_t snap_idx = kc > 0 ? c0 / kc : 0;
         // this lane's row of a stmatrix: tokens (0-7 | 8-15) x channels (0-7 | 8-15) of a block
-        const int orow = 32 * hf + (lane & 7) + ((lane >> 4) << 3), opiece = 4 * qd + ((lane >> 3) & 1);
-        const uint32_t obase = smem_u32(sm + kOffO);
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((s.start + (tid >> 4)) * a.H + h) * D + (tid & 15) * 8;
-        const int64_t tstride = a.H * D;
-        for (int c = 0; c < nch && ok; ++c, out += C * tstride) {
+        const int orow = 32 * hf + (lane & 7) + ((lane >> 4) << 3), opiece = (4 * qd & 7) + ((lane >> 3) & 1);
+        const uint32_t obase = smem_u32(sm + kOffO) + (uint32_t)(qd >> 1) * 8192u;
+        for (int c = 0; c < nch && ok; ++c) {
             const uint32_t par = (c >> 1) & 1;
             const Factors &fac = ring[c % kRing];
             ok = warp_wait(&bars.fac[c % kRing], (c / kRing) & 1);
@@ -314,7 +319,8 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             tc_fence_before();
             mbar_arrive(&bars.ds_read);
-            ok = warp_wait(&bars.o[c & 1], par);
+            if (c > 1) ok = warp_wait(&bars.out_empty[c & 1], par ^ 1);
+            ok = ok && warp_wait(&bars.o[c & 1], par);
             if (!ok) break;
             tc_fence_after();
             // o = scale 2^G O, rounded, turned from channel rows to token rows
@@ -329,20 +335,14 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     const float2 e0 = *reinterpret_cast<const float2 *>(fac.e + 32 * hf + 8 * n + 2 * (lane & 3));
                     const float2 e1 = *reinterpret_cast<const float2 *>(fac.e + 32 * hf + 8 * n + 8 + 2 * (lane & 3));
                     const float *y = x + 4 * n;
-                    stsm_x4_trans(ob + (uint32_t)(orow + 8 * n) * 256u + (((uint32_t)(opiece + 2 * m) ^ (uint32_t)(orow & 7)) << 4),
+                    stsm_x4_trans(ob + (uint32_t)(orow + 8 * n) * 128u + (((uint32_t)(opiece + 2 * m) ^ (uint32_t)(orow & 7)) << 4),
                                   pack_bf16(y[0] * e0.x, y[1] * e0.y), pack_bf16(y[2] * e0.x, y[3] * e0.y),
                                   pack_bf16(y[4] * e1.x, y[5] * e1.y), pack_bf16(y[6] * e1.x, y[7] * e1.y));
                 }
             }
             publish();  // of the next chunk; O is read too
-            named_bar_sync(1, 256);
-            const int L = (int)(s.len - (int64_t)c * C < C ? s.len - (int64_t)c * C : C);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // a token's 256 bytes by 16 lanes
-                const int t = (tid >> 4) + 16 * i;
-                const uint4 y = ld_shared_v4(ob + (uint32_t)t * 256u + (((uint32_t)(tid & 15) ^ (uint32_t)(t & 7)) << 4));
-                if (t < L) *reinterpret_cast<uint4 *>(out + 16 * i * tstride) = y;
-            }
+            fence_async_smem();
+            mbar_arrive(&bars.out_full[c & 1]);
             if (kc > 0 && --snap_left == 0) {
                 snap_left = kc;
                 if (snap_idx < a.n_snap) {
@@ -408,8 +408,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
     } else if (warp < kIssuer) {
         // ------------------------------------------------------------------
-        // P: query tokens 16 w .. 16 w + 15, of which a lane holds two (i0, i0 + 8).  Warp 12
-        // forms the gates' factors, two chunks ahead (two tokens per lane).
+        // P: query tokens 16 w .. 16 w + 15, of which a lane holds two (i0, i0 + 8).
         // ------------------------------------------------------------------
         const int w = warp - 12, i0 = 16 * w + (lane >> 2), j0 = 2 * (lane & 3);
         uint8_t *P = sm + kOffP;
@@ -421,45 +420,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             *reinterpret_cast<uint4 *>(P + (i >> 7) * 8192 + (16 * w + ((i >> 3) & 15)) * 128 + (i & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
-        const float gh = fixed ? a.g[h] * kLog2e : 0.f;
-        auto load_gate = [&](int c) {
-            const int64_t t = (int64_t)c * C + 2 * lane;
-            float2 g = make_float2(0.f, 0.f);
-            if (t < s.len) g.x = fixed ? gh : a.g[(s.start + t) * a.H + h] * kLog2e;
-            if (t + 1 < s.len) g.y = fixed ? gh : a.g[(s.start + t + 1) * a.H + h] * kLog2e;
-            return g;
-        };
-        float2 g = make_float2(0.f, 0.f), fixed_decay = make_float2(0.f, 0.f);
-        if (w == 0 && nch > 0) {
-            g = load_gate(0);
-            if (fixed) fixed_decay = exp2_pair((double)a.g[h] * 1.4426950408889634074 * C);
-        }
-        for (int c = -2; c < nch && ok; ++c) {
-            if (w == 0 && c + 2 < nch) {
-                // The slot's last readers, of chunk c - 6, are done: O of chunk c - 3 was formed
-                // (this warp waited for it), after O of chunk c - 4 was read.
-                const int cf = c + 2;
-                Factors &fac = ring[cf % kRing];
-                float2 G, after;
-                float total;
-                scan_gates(g.x, g.y, lane, G, after, total);
-                const bool far = !(total > kFarDecay);
-                *reinterpret_cast<float2 *>(&fac.G[2 * lane]) = G;
-                *reinterpret_cast<float2 *>(&fac.f[2 * lane]) = make_float2(ex2(-G.x), ex2(-G.y));
-                *reinterpret_cast<float2 *>(&fac.w[2 * lane]) = make_float2(ex2(after.x), ex2(after.y));
-                *reinterpret_cast<float2 *>(&fac.e[2 * lane]) =
-                    far ? make_float2(1.f, 1.f) : make_float2(a.scale * ex2(G.x), a.scale * ex2(G.y));
-                if (lane == 0) {
-                    const int64_t left = s.len - (int64_t)cf * C;
-                    fac.far = far;
-                    fac.decay = !fixed ? make_float2(ex2(total), 0.f)
-                                       : (left >= C ? fixed_decay
-                                                    : exp2_pair((double)a.g[h] * 1.4426950408889634074 * (double)left));
-                }
-                mbar_arrive(&bars.fac[cf % kRing]);
-                if (cf + 1 < nch) g = load_gate(cf + 1);
-            }
-            if (c < 0) continue;
+        for (int c = 0; c < nch && ok; ++c) {
             const Factors &fac = ring[c % kRing];
             ok = warp_wait(&bars.fac[c % kRing], (c / kRing) & 1);
             ok = ok && warp_wait(&bars.qk, c & 1);
@@ -514,44 +475,11 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             fence_async_smem();
             mbar_arrive(&bars.p[c & 1]);
         }
-    } else {
+    } else if (warp == kIssuer) {
         // ------------------------------------------------------------------
-        // Loads and MMAs
+        // MMAs
         // ------------------------------------------------------------------
         const uint32_t base = smem_u32(sm);
-        const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
-        auto load = [&](int c) {
-            if (lane == 0) {
-                uint8_t *st = sm + (c % kStages) * kStage;
-                uint64_t *bar = &bars.full[c % kStages];
-                const int32_t row = (int32_t)(s.start + (int64_t)c * C);
-                mbar_arrive_expect_tx(bar, kStage);
-#pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    tma_load_3d(st + kStQ + i * kHalfQK, &mq, 64 * i, hq, row, bar);
-                    tma_load_3d(st + kStK + i * kHalfQK, &mk, 64 * i, hq, row, bar);
-                    tma_load_3d(st + kStV + i * kHalfV, &mv, 64 * i, hv, row, bar);
-                }
-            }
-            issued = c + 1;
-            __syncwarp();
-        };
-        auto issue_qk = [&](int c) {
-            const uint32_t st = base + (c % kStages) * kStage;
-            const uint64_t aq = sdesc_sw128(st + kStQ, 16, 1024), bk = sdesc_sw128(st + kStK, 16, 1024);
-#pragma unroll 4
-            for (int kk = 0; kk < 8; ++kk) {
-                const uint64_t at = (uint64_t)(((kk >> 2) * kHalfQK + (kk & 3) * 32) >> 4);
-                mma_bf16_ss(tm + kTmQK, aq + at, bk + at, idesc_bf16(64, 64, 0, 0), kk > 0);
-            }
-            mma_commit_warp(&bars.qk);
-        };
-        if (lane == 0) {
-            prefetch_tmap(&mq);
-            prefetch_tmap(&mk);
-            prefetch_tmap(&mv);
-        }
-        for (int c = 0; c < 2 && c < nch; ++c) load(c);
         for (int c = -1; c < nch && ok; ++c) {
             const uint32_t par = c & 1, st = base + (c % kStages) * kStage;
             if (c >= 0) {  // dS
@@ -567,18 +495,24 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                                 i > 0);
                 mma_commit_warp(&bars.ds[par]);
             }
-            if (c + 1 < nch) {
-                ok = warp_wait(&bars.full[(c + 1) % kStages], ((c + 1) / kStages) & 1);
+            if (c + 1 < nch) {  // QK of the next chunk
+                const int stage = (c + 1) % kStages;
+                ok = warp_wait(&bars.full[stage], ((c + 1) / kStages) & 1);
                 if (c >= 0) ok = ok && warp_wait(&bars.qk_read, par);
                 if (!ok) break;
                 tc_fence_after();
-                issue_qk(c + 1);
+                const uint32_t sn = base + stage * kStage;
+                const uint64_t aq = sdesc_sw128(sn + kStQ, 16, 1024), bk = sdesc_sw128(sn + kStK, 16, 1024);
+#pragma unroll 4
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint64_t at = (uint64_t)(((kk >> 2) * kHalfQK + (kk & 3) * 32) >> 4);
+                    mma_bf16_ss(tm + kTmQK, aq + at, bk + at, idesc_bf16(64, 64, 0, 0), kk > 0);
+                }
+                mma_commit_warp(&bars.qk);
             }
             if (c >= 0) {  // O
                 ok = warp_wait(&bars.state, par);  // S0 in place, the previous chunk's O read
-                if (!ok) break;
-                if (c + 2 < nch) load(c + 2);  // into the previous chunk's stage: all its products are done
-                ok = warp_wait(&bars.p[par], (c >> 1) & 1);
+                ok = ok && warp_wait(&bars.p[par], (c >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t bq = sdesc_sw128(st + kStQ, 16, 1024);
@@ -592,7 +526,101 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     mma_bf16_ss(tm + kTmO, av + (uint64_t)((kk * 2048) >> 4), bp + (uint64_t)((kk * 32) >> 4),
                                 idesc_bf16(128, 64, 1, 0), 1);
                 mma_commit_warp(&bars.o[par]);
+                mma_commit_warp(&bars.empty[c % kStages]);
             }
+        }
+    } else if (warp == kLoader) {
+        if (lane == 0) {
+            prefetch_tmap(&mq);
+            prefetch_tmap(&mk);
+            prefetch_tmap(&mv);
+            const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
+            for (int c = 0; c < nch; ++c) {
+                const int stage = c % kStages;
+                if (c >= kStages && !(ok = mbar_wait(&bars.empty[stage], ((c / kStages) & 1) ^ 1))) break;
+                uint8_t *st = sm + stage * kStage;
+                uint64_t *bar = &bars.full[stage];
+                const int32_t row = (int32_t)(s.start + (int64_t)c * C);
+                mbar_arrive_expect_tx(bar, kStage);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    tma_load_3d(st + kStQ + i * kHalfQK, &mq, 64 * i, hq, row, bar);
+                    tma_load_3d(st + kStK + i * kHalfQK, &mk, 64 * i, hq, row, bar);
+                    tma_load_3d(st + kStV + i * kHalfV, &mv, 64 * i, hv, row, bar);
+                }
+                issued = c + 1;
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        issued = __shfl_sync(0xffffffffu, issued, 0);
+    } else if (warp == kStorer) {
+        const int32_t hv = (int32_t)h;
+        for (int c = 0; c < nch && ok; ++c) {
+            ok = warp_wait(&bars.out_full[c & 1], (c >> 1) & 1);
+            if (!ok) break;
+            const uint8_t *o = sm + kOffO + (c & 1) * 16384;
+            const int64_t row = s.start + (int64_t)c * C, left = s.len - (int64_t)c * C;
+            if (left >= C) {
+                if (lane == 0) {
+                    tma_store_3d(&mo, o, 0, hv, (int32_t)row);
+                    tma_store_3d(&mo, o + 8192, 64, hv, (int32_t)row);
+                    bulk_commit();
+                    bulk_wait_read();
+                    mbar_arrive(&bars.out_empty[c & 1]);
+                }
+            } else {  // rows behind the sequence stay as they are
+                __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.out) + (row * a.H + h) * D;
+                for (int i = lane; i < (int)left * 16; i += 32) {
+                    const int t = i >> 4, p = i & 15;
+                    *reinterpret_cast<uint4 *>(to + t * a.H * D + 8 * p) =
+                        *reinterpret_cast<const uint4 *>(o + (p >> 3) * 8192 + sw128_offset(t, p & 7));
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------
+        // The gates' factors, two tokens per lane
+        // ------------------------------------------------------------------
+        const float gh = fixed ? a.g[h] * kLog2e : 0.f;
+        auto load_gate = [&](int c) {
+            const int64_t t = (int64_t)c * C + 2 * lane;
+            float2 g = make_float2(0.f, 0.f);
+            if (t < s.len) g.x = fixed ? gh : a.g[(s.start + t) * a.H + h] * kLog2e;
+            if (t + 1 < s.len) g.y = fixed ? gh : a.g[(s.start + t + 1) * a.H + h] * kLog2e;
+            return g;
+        };
+        float2 g = make_float2(0.f, 0.f), next = g, fixed_decay = g;
+        if (nch > 0) g = load_gate(0);
+        if (nch > 1) next = load_gate(1);
+        if (fixed) fixed_decay = exp2_pair((double)a.g[h] * 1.4426950408889634074 * C);
+        for (int c = 0; c < nch; ++c) {
+            // Three chunks ahead at most: O of chunk c - 3 is formed, so O of chunk c - 4 was read,
+            // and the slot's last readers (chunk c - 8) are done.
+            if (c >= kStages) ok = warp_wait(&bars.empty[c % kStages], ((c / kStages) & 1) ^ 1);
+            if (!ok) break;
+            Factors &fac = ring[c % kRing];
+            float2 G, after;
+            float total;
+            scan_gates(g.x, g.y, lane, G, after, total);
+            g = next;
+            if (c + 2 < nch) next = load_gate(c + 2);
+            const bool far = !(total > kFarDecay);
+            *reinterpret_cast<float2 *>(&fac.G[2 * lane]) = G;
+            *reinterpret_cast<float2 *>(&fac.f[2 * lane]) = make_float2(ex2(-G.x), ex2(-G.y));
+            *reinterpret_cast<float2 *>(&fac.w[2 * lane]) = make_float2(ex2(after.x), ex2(after.y));
+            *reinterpret_cast<float2 *>(&fac.e[2 * lane]) =
+                far ? make_float2(1.f, 1.f) : make_float2(a.scale * ex2(G.x), a.scale * ex2(G.y));
+            if (lane == 0) {
+                const int64_t left = s.len - (int64_t)c * C;
+                fac.far = far;
+                fac.decay = !fixed ? make_float2(ex2(total), 0.f)
+                                   : (left >= C ? fixed_decay
+                                                : exp2_pair((double)a.g[h] * 1.4426950408889634074 * (double)left));
+            }
+            mbar_arrive(&bars.fac[c % kRing]);
         }
     }
     __syncwarp();
@@ -600,9 +628,10 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         // A wait gave up: record it.  Every other role's next wait gives up too (it waits,
         // directly or not, for this one), so all of them get here.
         if (lane == 0) flag_error(a.status, GDN_DEV_TIMEOUT_SCAN);
-        if (warp == kIssuer) {  // loads and MMAs still in flight
+        if (warp == kLoader)  // loads and MMAs still in flight
             for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
                 warp_wait(&bars.full[j % kStages], (j / kStages) & 1);
+        if (warp == kIssuer) {
             mma_commit_warp(&bars.drain);
             warp_wait(&bars.drain, 0);
         }
@@ -860,15 +889,17 @@ gdn_status make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t H) {
 gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s) {
     const int64_t grid = p.slots * p.H, sgrid = p.sslots * p.parts * p.H;
     if (grid > 0x7fffffffLL || sgrid > 0x7fffffffLL) return fail(GDN_ERR_UNSUPPORTED, "grid too large");
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     memset(&mq, 0, sizeof mq);
     memset(&mk, 0, sizeof mk);
     memset(&mv, 0, sizeof mv);
+    memset(&mo, 0, sizeof mo);
     gdn_status st = GDN_OK;
     if (p.rows > 0) {
         if ((st = make_map(&mq, a.q, p.rows, a.Hk)) != GDN_OK) return st;
         if ((st = make_map(&mk, a.k, p.rows, a.Hk)) != GDN_OK) return st;
         if ((st = make_map(&mv, a.v, p.rows, p.H)) != GDN_OK) return st;
+        if ((st = make_map(&mo, a.out, p.rows, p.H)) != GDN_OK) return st;
     }
     static const cudaError_t attr = [] {
         const cudaError_t e = cudaFuncSetAttribute(gdn_linattn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem);
@@ -889,7 +920,7 @@ gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s) {
     {
         log_launch("gdn_linattn_tc", dim3((unsigned)grid), dim3(kOutThreads), kOutSmem);
         LaunchScope ls("gdn_linattn_tc", s);
-        gdn_linattn_tc<<<(unsigned)grid, kOutThreads, kOutSmem, s>>>(mq, mk, mv, a, p.fixed_gate);
+        gdn_linattn_tc<<<(unsigned)grid, kOutThreads, kOutSmem, s>>>(mq, mk, mv, mo, a, p.fixed_gate);
     }
     return check_launch("gdn_linattn_tc");
 }
