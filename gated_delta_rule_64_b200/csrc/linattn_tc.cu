@@ -136,6 +136,42 @@ __device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t a, uint32_
                  : "memory");
 }
 
+// Four MMAs of a K loop in one go, by one elected lane: operands A_STEP / B_STEP apart (bytes / 16
+// of a shared-memory operand, columns of one in TMEM); the first adds to D if `add`, the
+// others always.  (The issuing warp shares its scheduler with four busy ones, so the
+// instructions around each MMA count: with an election and a predicate of its own for
+// every MMA the warp needed about 80 cycles each.)
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.u32 a1, %1, %5;\n\tadd.u32 a2, %1, 2 * %5;\n\tadd.u32 a3, %1, 3 * %5;\n\t"
+        "add.u64 b1, %2, %6;\n\tadd.u64 b2, %2, 2 * %6;\n\tadd.u64 b3, %2, 3 * %6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add), "n"(A_STEP), "n"(B_STEP)
+        : "memory");
+}
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.u64 a1, %1, %5;\n\tadd.u64 a2, %1, 2 * %5;\n\tadd.u64 a3, %1, 3 * %5;\n\t"
+        "add.u64 b1, %2, %6;\n\tadd.u64 b2, %2, 2 * %6;\n\tadd.u64 b3, %2, 3 * %6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add), "n"(A_STEP), "n"(B_STEP)
+        : "memory");
+}
+
 // Two bf16 values (low half first) times their weights, cut into three bf16 pairs whose sum is the
 // fp32 product exactly: 24 significant bits are eight, eight and eight, each cut off.
 __device__ __forceinline__ void split_terms(uint32_t v, float2 w, uint32_t &t0, uint32_t &t1, uint32_t &t2) {
@@ -489,10 +525,8 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 tc_fence_after();
                 const uint64_t bk = sdesc_sw128(st + kStK, kHalfQK, 1024);
                 const uint32_t t = tm + kTmT + 96 * par;
-#pragma unroll 4
-                for (int i = 0; i < 12; ++i)
-                    mma_bf16_ts(tm + kTmS, t + 8 * i, bk + (uint64_t)(((i & 3) * 2048) >> 4), idesc_bf16(128, 128, 0, 1),
-                                i > 0);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) mma4_ts<8, 128>(tm + kTmS, t + 32 * k, bk, idesc_bf16(128, 128, 0, 1), k > 0);
                 mma_commit_warp(&bars.ds[par]);
             }
             if (c + 1 < nch) {  // QK of the next chunk
@@ -503,11 +537,9 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 tc_fence_after();
                 const uint32_t sn = base + stage * kStage;
                 const uint64_t aq = sdesc_sw128(sn + kStQ, 16, 1024), bk = sdesc_sw128(sn + kStK, 16, 1024);
-#pragma unroll 4
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint64_t at = (uint64_t)(((kk >> 2) * kHalfQK + (kk & 3) * 32) >> 4);
-                    mma_bf16_ss(tm + kTmQK, aq + at, bk + at, idesc_bf16(64, 64, 0, 0), kk > 0);
-                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    mma4_ss<2, 2>(tm + kTmQK, aq + i * (kHalfQK >> 4), bk + i * (kHalfQK >> 4), idesc_bf16(64, 64, 0, 0), i);
                 mma_commit_warp(&bars.qk);
             }
             if (c >= 0) {  // O
@@ -517,14 +549,10 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 tc_fence_after();
                 const uint64_t bq = sdesc_sw128(st + kStQ, 16, 1024);
                 const uint64_t av = sdesc_sw128(st + kStV, kHalfV, 1024), bp = sdesc_sw128(base + kOffP + par * 8192, 16, 1024);
-#pragma unroll 4
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ts(tm + kTmO, tm + kTmA + kk * 8, bq + (uint64_t)(((kk >> 2) * kHalfQK + (kk & 3) * 32) >> 4),
-                                idesc_bf16(128, 64, 0, 0), kk > 0);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ss(tm + kTmO, av + (uint64_t)((kk * 2048) >> 4), bp + (uint64_t)((kk * 32) >> 4),
-                                idesc_bf16(128, 64, 1, 0), 1);
+                for (int i = 0; i < 2; ++i)
+                    mma4_ts<8, 2>(tm + kTmO, tm + kTmA + 32 * i, bq + i * (kHalfQK >> 4), idesc_bf16(128, 64, 0, 0), i);
+                mma4_ss<128, 2>(tm + kTmO, av, bp, idesc_bf16(128, 64, 1, 0), 1);
                 mma_commit_warp(&bars.o[par]);
                 mma_commit_warp(&bars.empty[c % kStages]);
             }
@@ -829,10 +857,7 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
             const uint64_t bk = sdesc_sw128(base + stage * kSsStage + kSsK, 8192, 1024);
 #pragma unroll
             for (int m = 0; m < 3; ++m)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(tm + kTmU, tm + kTmUT + 32 * m + 8 * kk, bk + (uint64_t)((kk * 2048) >> 4),
-                                idesc_bf16(128, 128, 0, 1), i > 0 || m > 0 || kk > 0);
+                mma4_ts<8, 128>(tm + kTmU, tm + kTmUT + 32 * m, bk, idesc_bf16(128, 128, 0, 1), i > 0 || m > 0);
             mma_commit_warp(&bars.ds);
             if (*(volatile int *)&s_last == i) break;
             // into the stage of chunk i - 1, whose products were done before these terms were stored
