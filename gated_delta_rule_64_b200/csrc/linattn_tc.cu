@@ -26,8 +26,11 @@
 //                into the fragment layout that a 16-lane TMEM store takes
 //   warps 12-15  P, 16 query tokens a warp (a 64-row product leaves 16 rows in each TMEM
 //                quarter), through the fragment layout too: TMEM to stmatrix
-//   warp 16      issues the MMAs          warp 17  issues the TMA loads (three stages of 48 KB)
-//   warp 18      stores the outputs       warp 19  the factors that come from the gates
+//   warp 16      issues the MMAs of dS, warp 17 those of QK and O: a wait of one does not hold
+//                up the other's products (one warp for all of them left the tensor pipe idle
+//                half of the time, at about 200 cycles a wait)
+//   warp 18      stores the outputs
+//   warp 19      TMA loads (three stages of 48 KB) and the factors that come from the gates
 // One block per SM: 205 KB of shared memory, all 512 TMEM columns.
 //
 // The loops of the roles are kept short on purpose: every scheduler runs a warp of each, and
@@ -136,6 +139,28 @@ __device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t a, uint32_
                  : "memory");
 }
 
+// 32 lanes x 32 columns, 32 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&x)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+}
+// Registers per thread of the calling warpgroup from here on.
+template <int N> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Four MMAs of a K loop in one go, by one elected lane: operands A_STEP / B_STEP apart (bytes / 16
 // of a shared-memory operand, columns of one in TMEM); the first adds to D if `add`, the
 // others always.  (The issuing warp shares its scheduler with four busy ones, so the
@@ -220,6 +245,10 @@ constexpr uint32_t kOutSmem = kOffO + 2 * 16384 + 1024;
 constexpr uint32_t kTmQK = 0, kTmO = 64, kTmS = 128, kTmA = 256, kTmT = 320;
 constexpr int kOutThreads = 20 * 32;
 constexpr int kRing = 8;  // chunks' gate factors
+// Registers per thread: 96 at launch (20 warps); the warps of the state take what P and the last
+// four give up, 2 * 128 + 96 + 64 + 64 = 5 * 96.
+constexpr int kRegState = 128, kRegP = 64, kRegRest = 64;
+static_assert(2 * kRegState + 96 + kRegP + kRegRest <= 5 * 96, "no more than the block was launched with");
 
 constexpr float kFarDecay = -100.f;  // log2 of a chunk's decay
 
@@ -237,7 +266,7 @@ struct OutBars {
     uint64_t out_full[2], out_empty[2];
     uint64_t qk, ds[2], o[2];                       // products done
     uint64_t state, terms[2], p[2], ds_read, qk_read;  // S0, V w and P ready; dS and QK read
-    uint64_t drain;
+    uint64_t drain[2];
 };
 
 __global__ void __launch_bounds__(kOutThreads, 1)
@@ -255,11 +284,11 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     if (!locate<false>(a, blockIdx.x / a.H, s)) return;
     if (!in_bounds(s.start >= 0 && s.start + s.len <= a.rows && s.n < a.N && h < a.H, a.status)) return;
     const int nch = (int)((s.len + C - 1) / C);
-    constexpr int kIssuer = 16, kLoader = 17, kStorer = 18;
+    constexpr int kIssuerS = 16, kIssuerO = 17, kStorer = 18, kLoader = 19;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 1);
+            mbar_init(&bars.empty[i], 2);  // both issuing warps
         }
         for (int i = 0; i < kRing; ++i) mbar_init(&bars.fac[i], 32);
         for (int i = 0; i < 2; ++i) {
@@ -274,10 +303,11 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         mbar_init(&bars.state, 256);
         mbar_init(&bars.ds_read, 256);
         mbar_init(&bars.qk_read, 128);
-        mbar_init(&bars.drain, 1);
+        mbar_init(&bars.drain[0], 1);
+        mbar_init(&bars.drain[1], 1);
         fence_mbar_init();
     }
-    if (warp == kIssuer) {
+    if (warp == kIssuerS) {
         tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
@@ -293,6 +323,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         // The state and the outputs: value channel v, key channels [64 hf, 64 hf + 64) of
         // the state, tokens [32 hf, 32 hf + 32) of the outputs.
         // ------------------------------------------------------------------
+        more_registers<kRegState>();
         const int qd = warp & 3, hf = warp >> 2, v = qd * 32 + lane;
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
         const int64_t srow = (int64_t)v * D + 64 * hf;
@@ -338,45 +369,48 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             tc_fence_after();
             const float2 d = fac.decay;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float x[16];
-                tmem_ld16(tm + lane_off + kTmS + 64 * hf + 16 * q, x);
+            for (int q = 0; q < 2; ++q) {
+                float x[32];
+                tmem_ld32(tm + lane_off + kTmS + 64 * hf + 32 * q, x);
                 tmem_wait_ld();
                 if (d.y != 0.f)  // (a fixed decay, in two floats)
 #pragma unroll
-                    for (int t = 0; t < 16; ++t) x[t] = fmaf(d.y, S[16 * q + t], x[t]);
+                    for (int t = 0; t < 32; ++t) x[t] = fmaf(d.y, S[32 * q + t], x[t]);
 #pragma unroll
-                for (int t = 0; t < 16; t += 2) {
-                    const float2 r = __ffma2_rn(make_float2(d.x, d.x), make_float2(S[16 * q + t], S[16 * q + t + 1]),
+                for (int t = 0; t < 32; t += 2) {
+                    const float2 r = __ffma2_rn(make_float2(d.x, d.x), make_float2(S[32 * q + t], S[32 * q + t + 1]),
                                                 make_float2(x[t], x[t + 1]));
-                    S[16 * q + t] = r.x;
-                    S[16 * q + t + 1] = r.y;
+                    S[32 * q + t] = r.x;
+                    S[32 * q + t + 1] = r.y;
                 }
             }
             tc_fence_before();
             mbar_arrive(&bars.ds_read);
-            if (c > 1) ok = warp_wait(&bars.out_empty[c & 1], par ^ 1);
-            ok = ok && warp_wait(&bars.o[c & 1], par);
+            ok = warp_wait(&bars.o[c & 1], par);
             if (!ok) break;
             tc_fence_after();
+            float x[2][16];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                tmem_ld_frag32(tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmO + 32 * hf, x[m]);
+            tmem_wait_ld();
+            publish();  // S of the next chunk; O is read too
             // o = scale 2^G O, rounded, turned from channel rows to token rows
+            if (c > 1) ok = warp_wait(&bars.out_empty[c & 1], par ^ 1);
+            if (!ok) break;
             const uint32_t ob = obase + (c & 1) * 16384;
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {  // channels 16 m ..
-                float x[16];
-                tmem_ld_frag32(tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmO + 32 * hf, x);
-                tmem_wait_ld();
+            for (int n = 0; n < 4; n += 2) {
+                const float2 e0 = *reinterpret_cast<const float2 *>(fac.e + 32 * hf + 8 * n + 2 * (lane & 3));
+                const float2 e1 = *reinterpret_cast<const float2 *>(fac.e + 32 * hf + 8 * n + 8 + 2 * (lane & 3));
 #pragma unroll
-                for (int n = 0; n < 4; n += 2) {
-                    const float2 e0 = *reinterpret_cast<const float2 *>(fac.e + 32 * hf + 8 * n + 2 * (lane & 3));
-                    const float2 e1 = *reinterpret_cast<const float2 *>(fac.e + 32 * hf + 8 * n + 8 + 2 * (lane & 3));
-                    const float *y = x + 4 * n;
+                for (int m = 0; m < 2; ++m) {  // channels 16 m ..
+                    const float *y = x[m] + 4 * n;
                     stsm_x4_trans(ob + (uint32_t)(orow + 8 * n) * 128u + (((uint32_t)(opiece + 2 * m) ^ (uint32_t)(orow & 7)) << 4),
                                   pack_bf16(y[0] * e0.x, y[1] * e0.y), pack_bf16(y[2] * e0.x, y[3] * e0.y),
                                   pack_bf16(y[4] * e1.x, y[5] * e1.y), pack_bf16(y[6] * e1.x, y[7] * e1.y));
                 }
             }
-            publish();  // of the next chunk; O is read too
             fence_async_smem();
             mbar_arrive(&bars.out_full[c & 1]);
             if (kc > 0 && --snap_left == 0) {
@@ -427,7 +461,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             tc_fence_after();
             const uint32_t from = terms_address(smem_u32(st + kStV) + (uint32_t)(w >> 1) * kHalfV, 0, 0, lane);
             const int piece = (w & 1) * 4;
-#pragma unroll 1
+#pragma unroll 2
             for (int i = 0; i < 8; ++i) {  // 16 channels x 16 tokens each
                 const int m = i >> 2, n = i & 3;
                 uint32_t t0[4], t1[4], t2[4];
@@ -442,10 +476,11 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             tc_fence_before();
             mbar_arrive(&bars.terms[c & 1]);
         }
-    } else if (warp < kIssuer) {
+    } else if (warp < kIssuerS) {
         // ------------------------------------------------------------------
         // P: query tokens 16 w .. 16 w + 15, of which a lane holds two (i0, i0 + 8).
         // ------------------------------------------------------------------
+        fewer_registers<kRegP>();
         const int w = warp - 12, i0 = 16 * w + (lane >> 2), j0 = 2 * (lane & 3);
         uint8_t *P = sm + kOffP;
         // this lane's row of a stmatrix: matrices (tokens 0-7, keys 0-7), (8-15, 0-7), (0-7, 8-15),
@@ -511,77 +546,63 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             fence_async_smem();
             mbar_arrive(&bars.p[c & 1]);
         }
-    } else if (warp == kIssuer) {
+    } else if (warp == kIssuerS) {
+        fewer_registers<kRegRest>();
         // ------------------------------------------------------------------
-        // MMAs
+        // MMAs of dS
         // ------------------------------------------------------------------
         const uint32_t base = smem_u32(sm);
-        for (int c = -1; c < nch && ok; ++c) {
-            const uint32_t par = c & 1, st = base + (c % kStages) * kStage;
-            if (c >= 0) {  // dS
-                if (c > 0) ok = warp_wait(&bars.ds_read, par ^ 1);
-                ok = ok && warp_wait(&bars.terms[par], (c >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t bk = sdesc_sw128(st + kStK, kHalfQK, 1024);
-                const uint32_t t = tm + kTmT + 96 * par;
+        for (int c = 0; c < nch; ++c) {
+            const uint32_t par = c & 1;
+            if (c > 0) ok = warp_wait(&bars.ds_read, par ^ 1);
+            ok = ok && warp_wait(&bars.terms[par], (c >> 1) & 1);  // (K has arrived with V)
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t bk = sdesc_sw128(base + (c % kStages) * kStage + kStK, kHalfQK, 1024);
+            const uint32_t t = tm + kTmT + 96 * par;
 #pragma unroll
-                for (int k = 0; k < 3; ++k) mma4_ts<8, 128>(tm + kTmS, t + 32 * k, bk, idesc_bf16(128, 128, 0, 1), k > 0);
-                mma_commit_warp(&bars.ds[par]);
-            }
-            if (c + 1 < nch) {  // QK of the next chunk
+            for (int k = 0; k < 3; ++k) mma4_ts<8, 128>(tm + kTmS, t + 32 * k, bk, idesc_bf16(128, 128, 0, 1), k > 0);
+            mma_commit_warp(&bars.ds[par]);
+            mma_commit_warp(&bars.empty[c % kStages]);
+        }
+    } else if (warp == kIssuerO) {
+        fewer_registers<kRegRest>();
+        // ------------------------------------------------------------------
+        // MMAs of QK, a chunk ahead, and of O
+        // ------------------------------------------------------------------
+        const uint32_t base = smem_u32(sm);
+        for (int c = -1; c < nch; ++c) {
+            const uint32_t par = c & 1;
+            if (c + 1 < nch) {
                 const int stage = (c + 1) % kStages;
                 ok = warp_wait(&bars.full[stage], ((c + 1) / kStages) & 1);
                 if (c >= 0) ok = ok && warp_wait(&bars.qk_read, par);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sn = base + stage * kStage;
-                const uint64_t aq = sdesc_sw128(sn + kStQ, 16, 1024), bk = sdesc_sw128(sn + kStK, 16, 1024);
+                const uint32_t st = base + stage * kStage;
+                const uint64_t aq = sdesc_sw128(st + kStQ, 16, 1024), bk = sdesc_sw128(st + kStK, 16, 1024);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     mma4_ss<2, 2>(tm + kTmQK, aq + i * (kHalfQK >> 4), bk + i * (kHalfQK >> 4), idesc_bf16(64, 64, 0, 0), i);
                 mma_commit_warp(&bars.qk);
             }
-            if (c >= 0) {  // O
-                ok = warp_wait(&bars.state, par);  // S0 in place, the previous chunk's O read
-                ok = ok && warp_wait(&bars.p[par], (c >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t bq = sdesc_sw128(st + kStQ, 16, 1024);
-                const uint64_t av = sdesc_sw128(st + kStV, kHalfV, 1024), bp = sdesc_sw128(base + kOffP + par * 8192, 16, 1024);
+            if (c < 0) continue;
+            ok = warp_wait(&bars.state, par);  // S0 in place, the previous chunk's O read
+            ok = ok && warp_wait(&bars.p[par], (c >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = base + (c % kStages) * kStage;
+            const uint64_t bq = sdesc_sw128(st + kStQ, 16, 1024);
+            const uint64_t av = sdesc_sw128(st + kStV, kHalfV, 1024), bp = sdesc_sw128(base + kOffP + par * 8192, 16, 1024);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    mma4_ts<8, 2>(tm + kTmO, tm + kTmA + 32 * i, bq + i * (kHalfQK >> 4), idesc_bf16(128, 64, 0, 0), i);
-                mma4_ss<128, 2>(tm + kTmO, av, bp, idesc_bf16(128, 64, 1, 0), 1);
-                mma_commit_warp(&bars.o[par]);
-                mma_commit_warp(&bars.empty[c % kStages]);
-            }
+            for (int i = 0; i < 2; ++i)
+                mma4_ts<8, 2>(tm + kTmO, tm + kTmA + 32 * i, bq + i * (kHalfQK >> 4), idesc_bf16(128, 64, 0, 0), i);
+            mma4_ss<128, 2>(tm + kTmO, av, bp, idesc_bf16(128, 64, 1, 0), 1);
+            mma_commit_warp(&bars.o[par]);
+            mma_commit_warp(&bars.empty[c % kStages]);
         }
-    } else if (warp == kLoader) {
-        if (lane == 0) {
-            prefetch_tmap(&mq);
-            prefetch_tmap(&mk);
-            prefetch_tmap(&mv);
-            const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
-            for (int c = 0; c < nch; ++c) {
-                const int stage = c % kStages;
-                if (c >= kStages && !(ok = mbar_wait(&bars.empty[stage], ((c / kStages) & 1) ^ 1))) break;
-                uint8_t *st = sm + stage * kStage;
-                uint64_t *bar = &bars.full[stage];
-                const int32_t row = (int32_t)(s.start + (int64_t)c * C);
-                mbar_arrive_expect_tx(bar, kStage);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    tma_load_3d(st + kStQ + i * kHalfQK, &mq, 64 * i, hq, row, bar);
-                    tma_load_3d(st + kStK + i * kHalfQK, &mk, 64 * i, hq, row, bar);
-                    tma_load_3d(st + kStV + i * kHalfV, &mv, 64 * i, hv, row, bar);
-                }
-                issued = c + 1;
-            }
-        }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        issued = __shfl_sync(0xffffffffu, issued, 0);
     } else if (warp == kStorer) {
+        fewer_registers<kRegRest>();
         const int32_t hv = (int32_t)h;
         for (int c = 0; c < nch && ok; ++c) {
             ok = warp_wait(&bars.out_full[c & 1], (c >> 1) & 1);
@@ -609,9 +630,16 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
+        fewer_registers<kRegRest>();
         // ------------------------------------------------------------------
-        // The gates' factors, two tokens per lane
+        // Loads, and the gates' factors, two tokens per lane
         // ------------------------------------------------------------------
+        const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
+        if (lane == 0) {
+            prefetch_tmap(&mq);
+            prefetch_tmap(&mk);
+            prefetch_tmap(&mv);
+        }
         const float gh = fixed ? a.g[h] * kLog2e : 0.f;
         auto load_gate = [&](int c) {
             const int64_t t = (int64_t)c * C + 2 * lane;
@@ -625,10 +653,25 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (nch > 1) next = load_gate(1);
         if (fixed) fixed_decay = exp2_pair((double)a.g[h] * 1.4426950408889634074 * C);
         for (int c = 0; c < nch; ++c) {
-            // Three chunks ahead at most: O of chunk c - 3 is formed, so O of chunk c - 4 was read,
-            // and the slot's last readers (chunk c - 8) are done.
-            if (c >= kStages) ok = warp_wait(&bars.empty[c % kStages], ((c / kStages) & 1) ^ 1);
+            const int stage = c % kStages;
+            if (c >= kStages) ok = warp_wait(&bars.empty[stage], ((c / kStages) & 1) ^ 1);
             if (!ok) break;
+            if (lane == 0) {
+                uint8_t *st = sm + stage * kStage;
+                uint64_t *bar = &bars.full[stage];
+                const int32_t row = (int32_t)(s.start + (int64_t)c * C);
+                mbar_arrive_expect_tx(bar, kStage);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    tma_load_3d(st + kStQ + i * kHalfQK, &mq, 64 * i, hq, row, bar);
+                    tma_load_3d(st + kStK + i * kHalfQK, &mk, 64 * i, hq, row, bar);
+                    tma_load_3d(st + kStV + i * kHalfV, &mv, 64 * i, hv, row, bar);
+                }
+            }
+            issued = c + 1;
+            __syncwarp();
+            // The factors' slot: O of chunk c - 3 is formed, so O of chunk c - 4 was read, and the
+            // slot's last readers (chunk c - 8) are done.
             Factors &fac = ring[c % kRing];
             float2 G, after;
             float total;
@@ -659,14 +702,14 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (warp == kLoader)  // loads and MMAs still in flight
             for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
                 warp_wait(&bars.full[j % kStages], (j / kStages) & 1);
-        if (warp == kIssuer) {
-            mma_commit_warp(&bars.drain);
-            warp_wait(&bars.drain, 0);
+        if (warp == kIssuerS || warp == kIssuerO) {
+            mma_commit_warp(&bars.drain[warp - kIssuerS]);
+            warp_wait(&bars.drain[warp - kIssuerS], 0);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kIssuer) tmem_dealloc(tm, 512);
+    if (warp == kIssuerS) tmem_dealloc(tm, 512);
 }
 
 // ===========================================================================
