@@ -37,6 +37,7 @@ struct Plan {
     int64_t parts, part_len;  // blocks of the state kernel per segment, and their tokens
     size_t off_status, off_tot, off_alive, off_state, total;
 };
+constexpr int64_t kMaxPart = 16384;  // tokens of a part (their weights lie in shared memory)
 Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed);
 
 struct Args {

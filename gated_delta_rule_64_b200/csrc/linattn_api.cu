@@ -83,10 +83,20 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
         p.slots = p.N * p.G;
         p.sslots = p.G > 1 ? p.slots : 0;
     }
-    // Parts of a segment's state (tensor cores): at most eight, of 16 chunks or more.  The
-    // CUDA-core state kernel takes a segment whole (it has d_v / 32 blocks for it already).
-    const int64_t chunks = p.seg / kChunk;
-    p.parts = p.tc ? (chunks / 16 < 1 ? 1 : (chunks / 16 > 8 ? 8 : chunks / 16)) : 1;
+    // Parts of a segment's state (tensor cores), of four chunks or more and kMaxPart tokens or
+    // fewer.  With a fixed gate a block sees at once whether its part reaches the segment's
+    // end, and heads whose state lasts work side by side: eight parts (long sequence of the
+    // benchmark: 505 us with one part, 142 us with eight).  With a gate per token it has to
+    // add up the gates behind its part first, 3 us even where it then has nothing to do, at
+    // one block per SM: about two blocks per SM in all (prefill: 35 us with eight parts, 16 us
+    // with two).  The CUDA-core state kernel takes a segment whole (it has d_v / 32 blocks for
+    // it already).
+    const int64_t chunks = p.seg / kChunk, least = (p.seg + kMaxPart - 1) / kMaxPart;
+    int64_t parts = p.fixed_gate ? 8 : (p.sslots > 0 ? 2 * sms / (p.sslots * p.H) : 1);
+    if (parts > 8) parts = 8;
+    if (parts > chunks / 4) parts = chunks / 4;
+    if (parts < least) parts = least;
+    p.parts = p.tc && parts > 1 ? parts : 1;
     p.part_len = (chunks + p.parts - 1) / p.parts * kChunk;
     size_t off = 0;
     p.off_status = off;
@@ -115,12 +125,16 @@ gdn_status gdn_linattn_workspace_size(const gdn_desc *d, int32_t num_seqs, size_
     if (st != GDN_OK) return st;
     if (!bytes) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
     if (num_seqs < 0) return fail(GDN_ERR_INVALID_ARG, "num_seqs < 0");
-    size_t total = d->B == 1 || num_seqs != d->B ? lin::make_plan(*d, num_seqs, true).total : 0;
-    if (num_seqs == d->B) {
-        const size_t fixed = lin::make_plan(*d, num_seqs, false).total;
-        total = fixed > total ? fixed : total;
+    // either gate kind; packed, and fixed-length where the number of sequences allows it
+    size_t total = 0;
+    for (int i = 0; i < 4; ++i) {
+        gdn_desc c = *d;
+        c.gate = i & 1 ? (int32_t)GDN_GATE_CONST : (int32_t)GDN_GATE_HEAD;
+        if (i & 2 ? num_seqs != d->B : d->B != 1) continue;
+        const size_t n = lin::make_plan(c, num_seqs, !(i & 2)).total;
+        total = n > total ? n : total;
     }
-    *bytes = total;
+    *bytes = total > kStatusBytes ? total : kStatusBytes;
     return GDN_OK;
 }
 

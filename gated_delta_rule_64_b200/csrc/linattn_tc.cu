@@ -153,6 +153,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&x)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
 }
+// Asynchronous copy of one float to shared memory (zero where `on` is false: nothing is read).
+__device__ __forceinline__ void async_copy4(float *dst, const float *src, bool on) {
+    const int bytes = on ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Registers per thread of the calling warpgroup from here on.
 template <int N> __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -245,9 +253,10 @@ constexpr uint32_t kOutSmem = kOffO + 2 * 16384 + 1024;
 constexpr uint32_t kTmQK = 0, kTmO = 64, kTmS = 128, kTmA = 256, kTmT = 320;
 constexpr int kOutThreads = 20 * 32;
 constexpr int kRing = 8;  // chunks' gate factors
+constexpr int kGateAhead = 6;
 // Registers per thread: 96 at launch (20 warps); the warps of the state take what P and the last
-// four give up, 2 * 128 + 96 + 64 + 64 = 5 * 96.
-constexpr int kRegState = 128, kRegP = 64, kRegRest = 64;
+// four give up, 2 * 136 + 96 + 56 + 56 = 5 * 96.
+constexpr int kRegState = 136, kRegP = 56, kRegRest = 56;
 static_assert(2 * kRegState + 96 + kRegP + kRegRest <= 5 * 96, "no more than the block was launched with");
 
 constexpr float kFarDecay = -100.f;  // log2 of a chunk's decay
@@ -277,6 +286,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     uint8_t *sm = align1024(smem_raw);
     __shared__ OutBars bars;
     __shared__ Factors ring[kRing];
+    __shared__ __align__(8) float gate_ring[kRing][C];  // gates as they are read, kGateAhead chunks ahead
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t h = blockIdx.x % a.H;
@@ -461,7 +471,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             tc_fence_after();
             const uint32_t from = terms_address(smem_u32(st + kStV) + (uint32_t)(w >> 1) * kHalfV, 0, 0, lane);
             const int piece = (w & 1) * 4;
-#pragma unroll 2
+#pragma unroll 4
             for (int i = 0; i < 8; ++i) {  // 16 channels x 16 tokens each
                 const int m = i >> 2, n = i & 3;
                 uint32_t t0[4], t1[4], t2[4];
@@ -641,17 +651,18 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             prefetch_tmap(&mv);
         }
         const float gh = fixed ? a.g[h] * kLog2e : 0.f;
-        auto load_gate = [&](int c) {
-            const int64_t t = (int64_t)c * C + 2 * lane;
-            float2 g = make_float2(0.f, 0.f);
-            if (t < s.len) g.x = fixed ? gh : a.g[(s.start + t) * a.H + h] * kLog2e;
-            if (t + 1 < s.len) g.y = fixed ? gh : a.g[(s.start + t + 1) * a.H + h] * kLog2e;
-            return g;
+        // A head's gates lie H floats apart, a memory sector each: they are asked for early.
+        auto ask_gates = [&](int c) {
+            if (c < nch && !fixed) {
+                const int64_t t = (int64_t)c * C + 2 * lane;
+                const float *p = a.g + (s.start + t) * a.H + h;
+                async_copy4(&gate_ring[c % kRing][2 * lane], t < s.len ? p : a.g, t < s.len);
+                async_copy4(&gate_ring[c % kRing][2 * lane + 1], t + 1 < s.len ? p + a.H : a.g, t + 1 < s.len);
+            }
+            async_commit();  // (a group per chunk, empty or not)
         };
-        float2 g = make_float2(0.f, 0.f), next = g, fixed_decay = g;
-        if (nch > 0) g = load_gate(0);
-        if (nch > 1) next = load_gate(1);
-        if (fixed) fixed_decay = exp2_pair((double)a.g[h] * 1.4426950408889634074 * C);
+        for (int c = 0; c < kGateAhead; ++c) ask_gates(c);
+        const float2 fixed_decay = fixed ? exp2_pair((double)a.g[h] * 1.4426950408889634074 * C) : make_float2(0.f, 0.f);
         for (int c = 0; c < nch; ++c) {
             const int stage = c % kStages;
             if (c >= kStages) ok = warp_wait(&bars.empty[stage], ((c / kStages) & 1) ^ 1);
@@ -672,12 +683,16 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             __syncwarp();
             // The factors' slot: O of chunk c - 3 is formed, so O of chunk c - 4 was read, and the
             // slot's last readers (chunk c - 8) are done.
+            ask_gates(c + kGateAhead);
+            async_wait<kGateAhead>();  // (a lane reads what it copied itself)
+            const int64_t left = s.len - (int64_t)c * C;
+            float2 g = *reinterpret_cast<const float2 *>(&gate_ring[c % kRing][2 * lane]);
+            g = fixed ? make_float2(2 * lane < left ? gh : 0.f, 2 * lane + 1 < left ? gh : 0.f)
+                      : make_float2(g.x * kLog2e, g.y * kLog2e);
             Factors &fac = ring[c % kRing];
             float2 G, after;
             float total;
             scan_gates(g.x, g.y, lane, G, after, total);
-            g = next;
-            if (c + 2 < nch) next = load_gate(c + 2);
             const bool far = !(total > kFarDecay);
             *reinterpret_cast<float2 *>(&fac.G[2 * lane]) = G;
             *reinterpret_cast<float2 *>(&fac.f[2 * lane]) = make_float2(ex2(-G.x), ex2(-G.y));
@@ -685,7 +700,6 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             *reinterpret_cast<float2 *>(&fac.e[2 * lane]) =
                 far ? make_float2(1.f, 1.f) : make_float2(a.scale * ex2(G.x), a.scale * ex2(G.y));
             if (lane == 0) {
-                const int64_t left = s.len - (int64_t)c * C;
                 fac.far = far;
                 fac.decay = !fixed ? make_float2(ex2(total), 0.f)
                                    : (left >= C ? fixed_decay
@@ -716,32 +730,75 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 // State kernel: what a part of a segment (not its sequence's last) adds to the state
 // at the segment's end
 // ===========================================================================
-// Backwards from the part's end, so that a token's weight is the sum of the gates after it
-// and the products add up in TMEM without a rescale; it stops where nothing earlier
-// reaches the segment's end.  A segment is cut into parts so that the heads whose
-// state lasts do not hold up the rest: their parts run side by side, and a part
-// behind which the decay has left nothing ends at once.
-// Warps 0-7: the terms of V w (32 value channels and 32 tokens a warp);
-// warp 8: loads and MMAs.  Two blocks per SM (98 KB, 256 TMEM columns each).
+// Backwards from the part's end: a token's weight is the sum of the gates after it, so the
+// products add up in TMEM without a rescale, and the kernel stops where nothing earlier
+// reaches the segment's end.  A segment is cut into parts so that the heads whose state
+// lasts do not hold up the rest: their parts run side by side, and a part behind which the
+// decay has left nothing ends at once.
+// The weights of the whole part are formed first, 512 tokens at a time by all warps; then
+// warps 0-7 make the terms of V w (32 value channels and 32 tokens a warp, two buffers in
+// TMEM) and warp 8 issues loads and MMAs.  One block per SM (352 TMEM columns).
 constexpr uint32_t kSsK = 0, kSsV = 16384, kSsStage = 32768;
-constexpr int kSsStages = 3;
-constexpr uint32_t kStateSmem = kSsStages * kSsStage + 1024;
+constexpr int kSsStages = 4;
+constexpr uint32_t kSsOffW = kSsStages * kSsStage;  // the part's weights, newest token last
 constexpr uint32_t kTmU = 0, kTmUT = 128;
 constexpr int kStateThreads = 9 * 32;
+constexpr int kSpan = 512;  // tokens of a step of the scan
 
 struct StateBars {
-    uint64_t full[kSsStages], terms, ds, drain;
+    uint64_t full[kSsStages], terms[2], ds[2], drain;
 };
 
-__global__ void __launch_bounds__(kStateThreads, 2)
+// Weights of the tokens [begin, end) of a segment, from the end backwards: wts[t - begin] = 2^{after +
+// gates behind t} for one head; stops after the step that brings the sum to kDead.
+// Returns the sum at the first token weighed, and in `first` that token.  256 threads or more
+// call it (the first 256 work), two tokens each.
+__device__ __forceinline__ float part_weights(const Args &a, const Slot &s, int64_t h, int64_t begin, int64_t end, float after,
+                                              float *wts, float *s_sum, int64_t &first) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int64_t t1 = end;
+    for (; t1 > begin && after > kDead; t1 -= kSpan) {
+        const int64_t t = t1 - kSpan + 2 * tid;  // this thread's tokens t, t + 1 (the last thread's are the newest)
+        float2 g = make_float2(0.f, 0.f);
+        if (tid < 256) {
+            if (t >= begin) g.x = a.g[(s.start + t) * a.H + h] * kLog2e;
+            if (t + 1 >= begin) g.y = a.g[(s.start + t + 1) * a.H + h] * kLog2e;
+        }
+        float sum = g.x + g.y;  // of this lane and the lanes above it
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_down_sync(0xffffffffu, sum, o);
+            if (lane + o < 32) sum += x;
+        }
+        __syncthreads();
+        if (warp < 8 && lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        float behind = after, all = 0.f;  // what follows this warp's tokens
+#pragma unroll
+        for (int w = 7; w >= 0; --w) {
+            if (w > warp) behind += s_sum[w];
+            all += s_sum[w];
+        }
+        if (wts && tid < 256) {
+            const float above = __shfl_down_sync(0xffffffffu, sum, 1);
+            const float b1 = behind + (lane < 31 ? above : 0.f);
+            if (t >= begin) wts[t - begin] = ex2(b1 + g.y);
+            if (t + 1 >= begin) wts[t + 1 - begin] = ex2(b1);
+        }
+        after += all;
+    }
+    first = t1 > begin ? t1 : begin;
+    return after;
+}
+
+__global__ void __launch_bounds__(kStateThreads, 1)
 gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Args a,
                      const bool fixed) {
     extern __shared__ unsigned char smem_raw[];
     uint8_t *sm = align1024(smem_raw);
+    float *wts = reinterpret_cast<float *>(sm + kSsOffW);
     __shared__ StateBars bars;
     __shared__ uint32_t tmem_base;
-    __shared__ int s_last;                     // index of the last chunk to add, once known
-    __shared__ __align__(16) float s_w[8][C];  // the chunk's weights, a copy per warp
     __shared__ float s_sum[8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t h = blockIdx.x % a.H, unit = blockIdx.x / a.H;
@@ -752,107 +809,106 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
         return;
     const int64_t begin = part * a.part_len;  // of the part, in the segment
     const int64_t end = begin + a.part_len < s.len ? begin + a.part_len : s.len;
-    const int nch = (int)((end - begin) / C);
     // the decay from the part's end to the segment's
     const double g64 = fixed ? (double)a.g[h] * 1.4426950408889634074 : 0.0;
-    float gap = fixed ? (float)(g64 * (double)(s.len - end)) : 0.f;
-    if (!fixed) {
-        constexpr int kSpan = 2048;
-        for (int64_t t1 = s.len; t1 > end && gap > kDead; t1 -= kSpan) {
-            float sum = 0.f;
-            if (warp < 8)
-                for (int64_t t = t1 - 1 - tid; t >= end && t >= t1 - kSpan; t -= 256) sum += a.g[(s.start + t) * a.H + h];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            __syncthreads();
-            if (warp < 8 && lane == 0) s_sum[warp] = sum;
-            __syncthreads();
-            float all = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) all += s_sum[w];
-            gap += all * kLog2e;
-        }
-    }
+    int64_t first = 0;
+    const float gap = fixed ? (float)(g64 * (double)(s.len - end))
+                            : part_weights(a, s, h, end, s.len, 0.f, nullptr, s_sum, first);
     const int64_t at = (s.ss * a.parts + part) * a.H + h;
-    const bool alive = nch > 0 && gap > kDead;
+    const bool alive = end > begin && gap > kDead;
     if (tid == 0) {
         a.alive[at] = alive ? 1 : 0;
         if (part == 0 && !alive) a.tot[s.ss * a.H + h] = (double)gap;
     }
     if (!alive) return;
+    const int64_t row_end = s.start + end;
+    const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
+    int issued = 0;  // (warp 8) chunks whose loads are issued
+    auto load = [&](int i) {  // chunk i from the part's end
+        if (lane == 0) {
+            uint8_t *st = sm + (i % kSsStages) * kSsStage;
+            uint64_t *bar = &bars.full[i % kSsStages];
+            const int32_t r = (int32_t)(row_end - (int64_t)(i + 1) * C);
+            mbar_arrive_expect_tx(bar, kSsStage);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                tma_load_3d(st + kSsK + k * 8192, &mk, 64 * k, hq, r, bar);
+                tma_load_3d(st + kSsV + k * 8192, &mv, 64 * k, hv, r, bar);
+            }
+        }
+        issued = i + 1;
+        __syncwarp();
+    };
+    const int most = (int)((end - begin) / C);
     if (tid == 0) {
         for (int i = 0; i < kSsStages; ++i) mbar_init(&bars.full[i], 1);
-        mbar_init(&bars.terms, 256);
-        mbar_init(&bars.ds, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.terms[i], 256);
+            mbar_init(&bars.ds[i], 1);
+        }
         mbar_init(&bars.drain, 1);
-        s_last = nch - 1;
         fence_mbar_init();
     }
     if (warp == 8) {
-        tmem_alloc(&tmem_base, 256);
+        tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (warp == 8)  // (on their way while the weights are formed)
+        for (int i = 0; i < kSsStages - 1 && i < most; ++i) load(i);
+    float reach;  // sum of the gates from the first chunk that is added on
+    if (fixed) {
+        // 2^{gap + g (tokens behind)}; nothing before the token where that is below 2^kDead
+        const double live = g64 < 0.0 ? ((double)kDead - (double)gap) / g64 : 1e18;
+        const int64_t keep = live < (double)(end - begin) ? (int64_t)live + 1 : end - begin;
+        first = end - keep;
+        const float g2 = (float)g64;
+        for (int64_t t = first / C * C - first + (int64_t)tid; t < keep; t += kStateThreads) {
+            const int64_t tok = first + t;
+            if (tok >= begin) wts[tok - begin] = ex2(gap + g2 * (float)(end - 1 - tok));
+        }
+        reach = (float)(g64 * (double)(s.len - begin));
+    } else {
+        reach = part_weights(a, s, h, begin, end, gap, wts, s_sum, first);
+    }
+    const int64_t first_chunk = first > begin ? (first - begin) / C : 0;
+    const int nch = most - (int)first_chunk;  // chunks to add, from the part's end (at least one)
+    // (tokens of the first one that the scan has not reached)
+    for (int64_t t = first_chunk * C + tid; t < first - begin; t += kStateThreads)
+        if (!fixed) wts[t] = 0.f;
+    __syncthreads();
     const uint32_t tm = tmem_base;
-    const int64_t row_end = s.start + end;
     bool ok = true;
-    int issued = 0, waited = 0;  // (warp 8) loads
+    int waited = 0;  // (warp 8) loads
     if (warp < 8) {
-        const float gh = fixed ? a.g[h] * kLog2e : 0.f;
-        auto load_gate = [&](int i) {  // chunk i from the part's end
-            if (fixed) return make_float2(gh, gh);
-            const float *p = a.g + (row_end - (int64_t)(i + 1) * C + 2 * lane) * a.H + h;
-            return make_float2(p[0] * kLog2e, p[a.H] * kLog2e);
-        };
         const int qd = warp & 3, hf = warp >> 2, v = qd * 32 + lane;
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
-        float *wts = s_w[warp];
-        float2 g = load_gate(0);
-        float after_chunk = gap;
-        int i = 0;
-        for (; i < nch; ++i) {
+        for (int i = 0; i < nch; ++i) {
             const int stage = i % kSsStages;
-            float2 G, after;
-            float total;
-            scan_gates(g.x, g.y, lane, G, after, total);
-            __syncwarp();
-            *reinterpret_cast<float2 *>(wts + 2 * lane) = make_float2(ex2(after.x + after_chunk), ex2(after.y + after_chunk));
-            __syncwarp();
-            after_chunk += total;
-            const bool last = i == nch - 1 || after_chunk <= kDead;  // (the same in every warp)
-            if (!last) g = load_gate(i + 1);
+            const float *w = wts + (most - 1 - i) * C + 32 * hf;
             ok = warp_wait(&bars.full[stage], (i / kSsStages) & 1);
-            if (!ok) break;
-            uint32_t t0[2][2][4], t1[2][2][4], t2[2][2][4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    channel_terms(terms_address(smem_u32(sm + stage * kSsStage + kSsV) + (uint32_t)(qd >> 1) * 8192u,
-                                                (qd & 1) * 4 + 2 * m, 32 * hf + 16 * n, lane),
-                                  wts + 32 * hf + 16 * n, lane, t0[m][n], t1[m][n], t2[m][n]);
-            if (i > 0) ok = warp_wait(&bars.ds, (i & 1) ^ 1);  // the previous chunk's products have read the terms
+            if (i >= 2) ok = ok && warp_wait(&bars.ds[i & 1], ((i >> 1) & 1) ^ 1);  // chunk i - 2 has used this buffer
             if (!ok) break;
             tc_fence_after();
+            const uint32_t half = smem_u32(sm + stage * kSsStage + kSsV) + (uint32_t)(qd >> 1) * 8192u;
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint32_t to = tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmUT + 16 * hf + 8 * n;
-                    tmem_st_frag8(to, t0[m][n]);
-                    tmem_st_frag8(to + 32, t1[m][n]);
-                    tmem_st_frag8(to + 64, t2[m][n]);
-                }
+            for (int k = 0; k < 4; ++k) {  // 16 channels x 16 tokens each
+                const int m = k >> 1, n = k & 1;
+                uint32_t t0[4], t1[4], t2[4];
+                channel_terms(terms_address(half, (qd & 1) * 4 + 2 * m, 32 * hf + 16 * n, lane), w + 16 * n, lane, t0, t1, t2);
+                const uint32_t to = tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmUT + 96 * (i & 1) + 16 * hf + 8 * n;
+                tmem_st_frag8(to, t0);
+                tmem_st_frag8(to + 32, t1);
+                tmem_st_frag8(to + 64, t2);
+            }
             tmem_wait_st();
-            if (last && tid == 0) s_last = i;
             tc_fence_before();
-            mbar_arrive(&bars.terms);
-            if (last) break;
+            mbar_arrive(&bars.terms[i & 1]);
         }
         if (ok) {
-            ok = warp_wait(&bars.ds, i & 1);  // the last chunk's products, and all before
+            ok = warp_wait(&bars.ds[(nch - 1) & 1], ((nch - 1) >> 1) & 1);  // the last chunk's products, and all before
             tc_fence_after();
         }
         if (ok) {
@@ -867,44 +923,28 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
                     *reinterpret_cast<float4 *>(U + 16 * q + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
             }
             // the segment's decay (once it is past kDead, how far past does not matter)
-            if (part == 0 && tid == 0) a.tot[s.ss * a.H + h] = fixed ? g64 * (double)s.len : (double)after_chunk;
+            if (part == 0 && tid == 0) a.tot[s.ss * a.H + h] = fixed ? g64 * (double)s.len : (double)reach;
         }
     } else {
         const uint32_t base = smem_u32(sm);
-        const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
-        auto load = [&](int i) {
-            const int stage = i % kSsStages;
-            if (lane == 0) {
-                uint8_t *st = sm + stage * kSsStage;
-                uint64_t *bar = &bars.full[stage];
-                const int32_t r = (int32_t)(row_end - (int64_t)(i + 1) * C);
-                mbar_arrive_expect_tx(bar, kSsStage);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    tma_load_3d(st + kSsK + k * 8192, &mk, 64 * k, hq, r, bar);
-                    tma_load_3d(st + kSsV + k * 8192, &mv, 64 * k, hv, r, bar);
-                }
-            }
-            issued = i + 1;
-            __syncwarp();
-        };
-        for (int i = 0; i < 2 && i < nch; ++i) load(i);
         for (int i = 0; i < nch; ++i) {
             const int stage = i % kSsStages;
             ok = warp_wait(&bars.full[stage], (i / kSsStages) & 1);
             if (!ok) break;
             waited = i + 1;
-            ok = warp_wait(&bars.terms, i & 1);
+            ok = warp_wait(&bars.terms[i & 1], (i >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t bk = sdesc_sw128(base + stage * kSsStage + kSsK, 8192, 1024);
+            const uint32_t t = tm + kTmUT + 96 * (i & 1);
 #pragma unroll
-            for (int m = 0; m < 3; ++m)
-                mma4_ts<8, 128>(tm + kTmU, tm + kTmUT + 32 * m, bk, idesc_bf16(128, 128, 0, 1), i > 0 || m > 0);
-            mma_commit_warp(&bars.ds);
-            if (*(volatile int *)&s_last == i) break;
-            // into the stage of chunk i - 1, whose products were done before these terms were stored
-            if (i + 2 < nch) load(i + 2);
+            for (int m = 0; m < 3; ++m) mma4_ts<8, 128>(tm + kTmU, t + 32 * m, bk, idesc_bf16(128, 128, 0, 1), i > 0 || m > 0);
+            mma_commit_warp(&bars.ds[i & 1]);
+            if (i + kSsStages - 1 < nch) {  // into the stage of chunk i - 1
+                if (i > 0) ok = warp_wait(&bars.ds[(i - 1) & 1], ((i - 1) >> 1) & 1);
+                if (!ok) break;
+                load(i + kSsStages - 1);
+            }
         }
     }
     __syncwarp();
@@ -919,7 +959,7 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
         for (int j = waited; j < issued; ++j) warp_wait(&bars.full[j % kSsStages], (j / kSsStages) & 1);
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tm, 256);
+    if (warp == 8) tmem_dealloc(tm, 512);
 }
 
 // ===========================================================================
@@ -969,18 +1009,19 @@ gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s) {
         if ((st = make_map(&mv, a.v, p.rows, p.H)) != GDN_OK) return st;
         if ((st = make_map(&mo, a.out, p.rows, p.H)) != GDN_OK) return st;
     }
+    const size_t state_smem = kSsOffW + (size_t)p.part_len * sizeof(float) + 1024;
     static const cudaError_t attr = [] {
         const cudaError_t e = cudaFuncSetAttribute(gdn_linattn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem);
         return e != cudaSuccess ? e
                                 : cudaFuncSetAttribute(gdn_linattn_state_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (int)kStateSmem);
+                                                       (int)(kSsOffW + kMaxPart * sizeof(float) + 1024));
     }();
     if (attr != cudaSuccess) return fail(GDN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(attr));
     if (sgrid > 0) {
         {
-            log_launch("gdn_linattn_state_tc", dim3((unsigned)sgrid), dim3(kStateThreads), kStateSmem);
+            log_launch("gdn_linattn_state_tc", dim3((unsigned)sgrid), dim3(kStateThreads), state_smem);
             LaunchScope ls("gdn_linattn_state_tc", s);
-            gdn_linattn_state_tc<<<(unsigned)sgrid, kStateThreads, kStateSmem, s>>>(mk, mv, a, p.fixed_gate);
+            gdn_linattn_state_tc<<<(unsigned)sgrid, kStateThreads, state_smem, s>>>(mk, mv, a, p.fixed_gate);
         }
         if ((st = check_launch("gdn_linattn_state_tc")) != GDN_OK) return st;
         if ((st = launch_combine(p, a, s)) != GDN_OK) return st;

@@ -37,7 +37,7 @@ enum { GDN_GATE_CONST = 2 };
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace gdn_linattn_chunk_fwd needs for d->T tokens in num_seqs
- * sequences (B when cu_seqlens is NULL); covers any packing. */
+ * sequences (B when cu_seqlens is NULL); covers any packing and both gate kinds. */
 gdn_status gdn_linattn_workspace_size(const gdn_desc *d, int32_t num_seqs, size_t *bytes);
 
 /* ---------------------------------------------------------------------------
