@@ -38,6 +38,7 @@ struct Plan {
     size_t off_status, off_tot, off_alive, off_state, total;
 };
 constexpr int64_t kMaxPart = 16384;  // tokens of a part (their weights lie in shared memory)
+constexpr int64_t kMostParts = 32;   // of a segment (the combine kernel keeps a bit for each)
 Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed);
 
 struct Args {

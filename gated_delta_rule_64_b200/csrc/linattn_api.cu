@@ -74,6 +74,8 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
     }
     const int64_t units = p.tc ? p.H : p.H * (p.dv / 32), wide = p.tc ? sms : 2 * sms;
     p.seg = choose_seg(p.N, units, d.T, p.rows, packed, wide);
+    // (a bound that only sequences of half a million tokens in one segment meet)
+    if (p.tc && p.seg > kMaxPart * kMostParts) p.seg = kMaxPart * kMostParts;
     if (packed) {
         p.G = 0;
         p.slots = p.rows / p.seg + p.N;

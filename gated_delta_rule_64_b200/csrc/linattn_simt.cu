@@ -286,41 +286,60 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a,
 
 // Start states of the segments of one sequence and head, each in the place of its first
 // part's U: S_{j+1} = 2^{tot_j} S_j + sum of the parts' U_j.  A thread chains four
-// elements; the next segment's U are in flight while the current one is added.
-constexpr int kCombThreads = 256;
+// elements.  What decides which U are read, and the decays, are fetched 32 segments at a
+// time by the whole block; the next segment's U are in flight while the current one is
+// added.
+constexpr int kCombThreads = 256, kCombSegs = 32, kCombParts = 8;
 __global__ void __launch_bounds__(kCombThreads) gdn_linattn_combine(const Args a, int64_t elems) {
+    __shared__ float2 s_decay[kCombSegs];
+    __shared__ uint32_t s_alive[kCombSegs];  // a bit per part (of the first kCombParts)
     const int64_t h = blockIdx.y, e = ((int64_t)blockIdx.z * kCombThreads + threadIdx.x) * 4;
-    if (e >= elems) return;
+    const int tid = threadIdx.x, parts = (int)a.parts;
     for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
         int64_t start, len;
         seq_bounds(a.cu, n, a.T, a.rows, start, len);
         const int64_t nseg = (len + a.seg - 1) / a.seg, ss = state_base(a, n);
         if (nseg < 2 || ss + nseg > a.sslots) continue;
-        const int parts = (int)a.parts;
         float *states = a.states + (ss * parts * a.H + h) * elems + e;
-        const int32_t *alive = a.alive + ss * parts * a.H + h;
-        const double *tot = a.tot + ss * a.H + h;
-        auto added = [&](int64_t j) {
-            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int i = 0; i < parts; ++i)
-                if (alive[(j * parts + i) * a.H]) {
-                    const float4 x = *reinterpret_cast<const float4 *>(states + (j * parts + i) * a.H * elems);
-                    u.x += x.x; u.y += x.y; u.z += x.z; u.w += x.w;
-                }
-            return u;
-        };
         float4 S = a.h0 ? *reinterpret_cast<const float4 *>(a.h0 + (n * a.H + h) * elems + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 u = added(0);
-        for (int64_t j = 0; j + 1 < nseg; ++j) {
-            const float4 next = j + 2 < nseg ? added(j + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float2 d = exp2_pair(tot[j * a.H]);
-            *reinterpret_cast<float4 *>(states + j * parts * a.H * elems) = S;
-            S.x = fmaf(d.x, S.x, fmaf(d.y, S.x, u.x));
-            S.y = fmaf(d.x, S.y, fmaf(d.y, S.y, u.y));
-            S.z = fmaf(d.x, S.z, fmaf(d.y, S.z, u.z));
-            S.w = fmaf(d.x, S.w, fmaf(d.y, S.w, u.w));
-            u = next;
+        for (int64_t j0 = 0; j0 + 1 < nseg; j0 += kCombSegs) {
+            const int m = (int)(nseg - 1 - j0 < kCombSegs ? nseg - 1 - j0 : kCombSegs);
+            __syncthreads();
+            if (tid < m) s_alive[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < m * parts; i += kCombThreads)
+                if (a.alive[((ss + j0) * parts + i) * a.H + h]) atomicOr(&s_alive[i / parts], 1u << (i % parts));
+            if (tid < m) s_decay[tid] = exp2_pair(a.tot[(ss + j0 + tid) * a.H + h]);
+            __syncthreads();
+            auto added = [&](int j) {
+                float4 x[kCombParts], u = make_float4(0.f, 0.f, 0.f, 0.f);
+                const uint32_t bits = s_alive[j];
+#pragma unroll
+                for (int i = 0; i < kCombParts; ++i)
+                    x[i] = bits >> i & 1 ? *reinterpret_cast<const float4 *>(states + ((j0 + j) * parts + i) * a.H * elems)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kCombParts; ++i) {
+                    u.x += x[i].x; u.y += x[i].y; u.z += x[i].z; u.w += x[i].w;
+                }
+                for (int i = kCombParts; i < parts; ++i)  // (very long segments)
+                    if (bits >> i & 1) {
+                        const float4 y = *reinterpret_cast<const float4 *>(states + ((j0 + j) * parts + i) * a.H * elems);
+                        u.x += y.x; u.y += y.y; u.z += y.z; u.w += y.w;
+                    }
+                return u;
+            };
+            float4 u = added(0);
+            for (int j = 0; j < m; ++j) {
+                const float4 next = j + 1 < m ? added(j + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float2 d = s_decay[j];
+                *reinterpret_cast<float4 *>(states + (j0 + j) * parts * a.H * elems) = S;
+                S.x = fmaf(d.x, S.x, fmaf(d.y, S.x, u.x));
+                S.y = fmaf(d.x, S.y, fmaf(d.y, S.y, u.y));
+                S.z = fmaf(d.x, S.z, fmaf(d.y, S.z, u.z));
+                S.w = fmaf(d.x, S.w, fmaf(d.y, S.w, u.w));
+                u = next;
+            }
         }
         *reinterpret_cast<float4 *>(states + (nseg - 1) * parts * a.H * elems) = S;
     }

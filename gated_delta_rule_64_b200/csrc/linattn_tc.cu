@@ -735,24 +735,25 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 // reaches the segment's end.  A segment is cut into parts so that the heads whose state
 // lasts do not hold up the rest: their parts run side by side, and a part behind which the
 // decay has left nothing ends at once.
-// The weights of the whole part are formed first, 512 tokens at a time by all warps; then
-// warps 0-7 make the terms of V w (32 value channels and 32 tokens a warp, two buffers in
-// TMEM) and warp 8 issues loads and MMAs.  One block per SM (352 TMEM columns).
+// The weights of the whole part are formed first, 1024 tokens at a time by warps 0-15; then
+// these make the terms of V w (32 value channels and 16 tokens a warp, two buffers in TMEM),
+// warp 16 issues the MMAs and warp 17 the loads.  One block per SM (320 TMEM columns).
 constexpr uint32_t kSsK = 0, kSsV = 16384, kSsStage = 32768;
 constexpr int kSsStages = 4;
 constexpr uint32_t kSsOffW = kSsStages * kSsStage;  // the part's weights, newest token last
 constexpr uint32_t kTmU = 0, kTmUT = 128;
-constexpr int kStateThreads = 9 * 32;
-constexpr int kSpan = 512;  // tokens of a step of the scan
+constexpr int kTermWarps = 16, kTermThreads = kTermWarps * 32;
+constexpr int kStateThreads = (kTermWarps + 2) * 32;
+constexpr int kSpan = 2 * kTermThreads;  // tokens of a step of the scan
 
 struct StateBars {
-    uint64_t full[kSsStages], terms[2], ds[2], drain;
+    uint64_t full[kSsStages], empty[kSsStages], terms[2], ds[2], drain;
 };
 
 // Weights of the tokens [begin, end) of a segment, from the end backwards: wts[t - begin] = 2^{after +
 // gates behind t} for one head; stops after the step that brings the sum to kDead.
-// Returns the sum at the first token weighed, and in `first` that token.  256 threads or more
-// call it (the first 256 work), two tokens each.
+// Returns the sum at the first token weighed, and in `first` that token.  The whole block
+// calls it; the first kTermThreads threads take two tokens each.
 __device__ __forceinline__ float part_weights(const Args &a, const Slot &s, int64_t h, int64_t begin, int64_t end, float after,
                                               float *wts, float *s_sum, int64_t &first) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -760,7 +761,7 @@ __device__ __forceinline__ float part_weights(const Args &a, const Slot &s, int6
     for (; t1 > begin && after > kDead; t1 -= kSpan) {
         const int64_t t = t1 - kSpan + 2 * tid;  // this thread's tokens t, t + 1 (the last thread's are the newest)
         float2 g = make_float2(0.f, 0.f);
-        if (tid < 256) {
+        if (tid < kTermThreads) {
             if (t >= begin) g.x = a.g[(s.start + t) * a.H + h] * kLog2e;
             if (t + 1 >= begin) g.y = a.g[(s.start + t + 1) * a.H + h] * kLog2e;
         }
@@ -771,15 +772,15 @@ __device__ __forceinline__ float part_weights(const Args &a, const Slot &s, int6
             if (lane + o < 32) sum += x;
         }
         __syncthreads();
-        if (warp < 8 && lane == 0) s_sum[warp] = sum;
+        if (warp < kTermWarps && lane == 0) s_sum[warp] = sum;
         __syncthreads();
         float behind = after, all = 0.f;  // what follows this warp's tokens
 #pragma unroll
-        for (int w = 7; w >= 0; --w) {
+        for (int w = kTermWarps - 1; w >= 0; --w) {
             if (w > warp) behind += s_sum[w];
             all += s_sum[w];
         }
-        if (wts && tid < 256) {
+        if (wts && tid < kTermThreads) {
             const float above = __shfl_down_sync(0xffffffffu, sum, 1);
             const float b1 = behind + (lane < 31 ? above : 0.f);
             if (t >= begin) wts[t - begin] = ex2(b1 + g.y);
@@ -799,12 +800,14 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
     float *wts = reinterpret_cast<float *>(sm + kSsOffW);
     __shared__ StateBars bars;
     __shared__ uint32_t tmem_base;
-    __shared__ float s_sum[8];
+    __shared__ float s_sum[kTermWarps];
+    constexpr int kIssuer = kTermWarps, kLoader = kTermWarps + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t h = blockIdx.x % a.H, unit = blockIdx.x / a.H;
-    const int64_t part = unit % a.parts;
+    // (the newest parts of all segments first: the blocks that find nothing to do come last)
+    const int64_t part = a.parts - 1 - unit / a.sslots;
     Slot s;
-    if (!locate<true>(a, unit / a.parts, s) || s.nseg < 2 || s.j == s.nseg - 1) return;
+    if (!locate<true>(a, unit % a.sslots, s) || s.nseg < 2 || s.j == s.nseg - 1) return;
     if (!in_bounds(s.start >= 0 && s.start + s.len <= a.rows && s.n < a.N && s.ss < a.sslots && s.len % C == 0, a.status))
         return;
     const int64_t begin = part * a.part_len;  // of the part, in the segment
@@ -821,14 +824,33 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
         if (part == 0 && !alive) a.tot[s.ss * a.H + h] = (double)gap;
     }
     if (!alive) return;
-    const int64_t row_end = s.start + end;
-    const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
-    int issued = 0;  // (warp 8) chunks whose loads are issued
+    const int most = (int)((end - begin) / C);
+    if (tid == 0) {
+        for (int i = 0; i < kSsStages; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.terms[i], kTermThreads);
+            mbar_init(&bars.ds[i], 1);
+        }
+        mbar_init(&bars.drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == kIssuer) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int issued = 0;  // (loader) chunks whose loads are issued
     auto load = [&](int i) {  // chunk i from the part's end
         if (lane == 0) {
             uint8_t *st = sm + (i % kSsStages) * kSsStage;
             uint64_t *bar = &bars.full[i % kSsStages];
-            const int32_t r = (int32_t)(row_end - (int64_t)(i + 1) * C);
+            const int32_t r = (int32_t)(s.start + end - (int64_t)(i + 1) * C);
+            const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
             mbar_arrive_expect_tx(bar, kSsStage);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -839,66 +861,45 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
         issued = i + 1;
         __syncwarp();
     };
-    const int most = (int)((end - begin) / C);
-    if (tid == 0) {
-        for (int i = 0; i < kSsStages; ++i) mbar_init(&bars.full[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.terms[i], 256);
-            mbar_init(&bars.ds[i], 1);
-        }
-        mbar_init(&bars.drain, 1);
-        fence_mbar_init();
-    }
-    if (warp == 8) {
-        tmem_alloc(&tmem_base, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 8)  // (on their way while the weights are formed)
-        for (int i = 0; i < kSsStages - 1 && i < most; ++i) load(i);
+    if (warp == kLoader)  // (on their way while the weights are formed)
+        for (int i = 0; i < kSsStages && i < most; ++i) load(i);
     float reach;  // sum of the gates from the first chunk that is added on
     if (fixed) {
         // 2^{gap + g (tokens behind)}; nothing before the token where that is below 2^kDead
         const double live = g64 < 0.0 ? ((double)kDead - (double)gap) / g64 : 1e18;
         const int64_t keep = live < (double)(end - begin) ? (int64_t)live + 1 : end - begin;
-        first = end - keep;
+        first = (end - keep) / C * C;
+        first = first > begin ? first : begin;
         const float g2 = (float)g64;
-        for (int64_t t = first / C * C - first + (int64_t)tid; t < keep; t += kStateThreads) {
-            const int64_t tok = first + t;
-            if (tok >= begin) wts[tok - begin] = ex2(gap + g2 * (float)(end - 1 - tok));
-        }
-        reach = (float)(g64 * (double)(s.len - begin));
+        for (int64_t t = first + tid; t < end; t += kStateThreads) wts[t - begin] = ex2(gap + g2 * (float)(end - 1 - t));
+        reach = 0.f;
     } else {
         reach = part_weights(a, s, h, begin, end, gap, wts, s_sum, first);
     }
-    const int64_t first_chunk = first > begin ? (first - begin) / C : 0;
-    const int nch = most - (int)first_chunk;  // chunks to add, from the part's end (at least one)
-    // (tokens of the first one that the scan has not reached)
-    for (int64_t t = first_chunk * C + tid; t < first - begin; t += kStateThreads)
-        if (!fixed) wts[t] = 0.f;
     __syncthreads();
+    // chunks to add, from the part's end: all those whose newest token still weighs something (at
+    // least one)
+    int skip = (int)((first - begin) / C);
+    while (skip < most - 1 && wts[skip * C + C - 1] == 0.f) ++skip;
+    const int nch = most - skip;
     const uint32_t tm = tmem_base;
     bool ok = true;
-    int waited = 0;  // (warp 8) loads
-    if (warp < 8) {
-        const int qd = warp & 3, hf = warp >> 2, v = qd * 32 + lane;
+    if (warp < kTermWarps) {
+        const int qd = warp & 3, tq = warp >> 2;  // channels 32 qd .., tokens 16 tq ..
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+        const uint32_t from = terms_address(smem_u32(sm + kSsV) + (uint32_t)(qd >> 1) * 8192u, (qd & 1) * 4, 16 * tq, lane);
         for (int i = 0; i < nch; ++i) {
             const int stage = i % kSsStages;
-            const float *w = wts + (most - 1 - i) * C + 32 * hf;
+            const float *w = wts + (most - 1 - i) * C + 16 * tq;
             ok = warp_wait(&bars.full[stage], (i / kSsStages) & 1);
             if (i >= 2) ok = ok && warp_wait(&bars.ds[i & 1], ((i >> 1) & 1) ^ 1);  // chunk i - 2 has used this buffer
             if (!ok) break;
             tc_fence_after();
-            const uint32_t half = smem_u32(sm + stage * kSsStage + kSsV) + (uint32_t)(qd >> 1) * 8192u;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // 16 channels x 16 tokens each
-                const int m = k >> 1, n = k & 1;
+            for (int m = 0; m < 2; ++m) {  // 16 channels x 16 tokens each
                 uint32_t t0[4], t1[4], t2[4];
-                channel_terms(terms_address(half, (qd & 1) * 4 + 2 * m, 32 * hf + 16 * n, lane), w + 16 * n, lane, t0, t1, t2);
-                const uint32_t to = tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmUT + 96 * (i & 1) + 16 * hf + 8 * n;
+                channel_terms((from + stage * kSsStage) ^ (uint32_t)(m << 5), w, lane, t0, t1, t2);
+                const uint32_t to = tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmUT + 96 * (i & 1) + 8 * tq;
                 tmem_st_frag8(to, t0);
                 tmem_st_frag8(to + 32, t1);
                 tmem_st_frag8(to + 64, t2);
@@ -912,11 +913,11 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
             tc_fence_after();
         }
         if (ok) {
-            float *U = a.states + at * (int64_t)(D * D) + (int64_t)v * D + 64 * hf;
+            float *U = a.states + at * (int64_t)(D * D) + (int64_t)(qd * 32 + lane) * D + 32 * tq;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 float x[16];
-                tmem_ld16(tm + lane_off + kTmU + 64 * hf + 16 * q, x);
+                tmem_ld16(tm + lane_off + kTmU + 32 * tq + 16 * q, x);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
@@ -925,41 +926,40 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
             // the segment's decay (once it is past kDead, how far past does not matter)
             if (part == 0 && tid == 0) a.tot[s.ss * a.H + h] = fixed ? g64 * (double)s.len : (double)reach;
         }
-    } else {
+    } else if (warp == kIssuer) {
         const uint32_t base = smem_u32(sm);
         for (int i = 0; i < nch; ++i) {
-            const int stage = i % kSsStages;
-            ok = warp_wait(&bars.full[stage], (i / kSsStages) & 1);
-            if (!ok) break;
-            waited = i + 1;
-            ok = warp_wait(&bars.terms[i & 1], (i >> 1) & 1);
+            ok = warp_wait(&bars.terms[i & 1], (i >> 1) & 1);  // (K has arrived with V)
             if (!ok) break;
             tc_fence_after();
-            const uint64_t bk = sdesc_sw128(base + stage * kSsStage + kSsK, 8192, 1024);
+            const uint64_t bk = sdesc_sw128(base + (i % kSsStages) * kSsStage + kSsK, 8192, 1024);
             const uint32_t t = tm + kTmUT + 96 * (i & 1);
 #pragma unroll
             for (int m = 0; m < 3; ++m) mma4_ts<8, 128>(tm + kTmU, t + 32 * m, bk, idesc_bf16(128, 128, 0, 1), i > 0 || m > 0);
             mma_commit_warp(&bars.ds[i & 1]);
-            if (i + kSsStages - 1 < nch) {  // into the stage of chunk i - 1
-                if (i > 0) ok = warp_wait(&bars.ds[(i - 1) & 1], ((i - 1) >> 1) & 1);
-                if (!ok) break;
-                load(i + kSsStages - 1);
-            }
+            mma_commit_warp(&bars.empty[i % kSsStages]);
+        }
+    } else {
+        for (int i = kSsStages; i < nch; ++i) {
+            ok = warp_wait(&bars.empty[i % kSsStages], ((i / kSsStages) & 1) ^ 1);
+            if (!ok) break;
+            load(i);
         }
     }
     __syncwarp();
     if (!ok) {
         if (lane == 0) flag_error(a.status, GDN_DEV_TIMEOUT_PREP);
-        if (warp == 8) {
+        if (warp == kIssuer) {
             mma_commit_warp(&bars.drain);
             warp_wait(&bars.drain, 0);
         }
     }
-    if (warp == 8)  // loads still in flight (chunks that the early end left out)
-        for (int j = waited; j < issued; ++j) warp_wait(&bars.full[j % kSsStages], (j / kSsStages) & 1);
+    if (warp == kLoader)  // loads that nobody has waited for: chunks left out, or all the last ones after a failed wait
+        for (int j = issued > kSsStages ? issued - kSsStages : 0; j < issued; ++j)
+            if (!ok || j >= nch) warp_wait(&bars.full[j % kSsStages], (j / kSsStages) & 1);
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tm, 512);
+    if (warp == kIssuer) tmem_dealloc(tm, 512);
 }
 
 // ===========================================================================
