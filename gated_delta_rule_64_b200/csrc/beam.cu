@@ -8,48 +8,57 @@
 // joins a request's slices: the normaliser of each beam in 64 bits, the scores of the
 // W * slices * K candidates, and the K best of those.
 //
-// The K best of a slice.  Every thread's best is known after the pass over its registers; the
-// K-th best T of the 256 thread bests (a binary search over the bits of its key by
-// one warp) is a lower bound of the slice's K-th best, and only the K threads whose best
-// is at least T can hold values above it.  Those values, at least K and on random logits
-// little more, go to shared memory, where each one's rank is the number of better
-// ones.  Keys are (value, lowest index first), all different, so ties need no care.
+// The K best, in both.  Every thread knows its best value; each of the eight warps finds the
+// R-th best of its 32, R = ceil(K / 8) (a few rounds of a warp-wide maximum).  At least
+// 8 R >= K values reach the least of those eight, T, so nothing below T can be among the K
+// best, and on random values little more than K reach it: they go to shared memory, where
+// each one's rank is the number of better ones.  Values are compared by their order bits and
+// then by index, lowest first.  Where too many reach T (long runs of equal values) the slice
+// falls back on the K-th best of the threads' (value, index) pairs, of which at most K
+// threads have one, and the join on K rounds of a block-wide maximum.
 //
 // Reordering.  A thread owns 16 bytes of every beam's row of one request: it reads the
 // parents' bytes of all beams that change, then writes them, so the move is in place
 // without a second buffer and rows that stay are neither read nor written.
 #include "linattn.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
 namespace lin {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kEach = 32;                     // logits of a thread
-constexpr int kSlice = kThreads * kEach;      // logits of a block
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxK = 64;
+constexpr int kEachMost = 32;  // logits of a thread of the first kernel: 32, or 8 where that leaves SMs idle
 
 // A value's bits, ordered as unsigned integers; NaN counts as -infinity.
 __device__ __forceinline__ uint32_t order_bits(float x) {
     if (x != x) x = -INFINITY;
-    if (x == 0.f) x = 0.f;  // -0 and 0 are equal
-    const uint32_t u = __float_as_uint(x);
+    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);  // -0 and 0 are equal
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-template <typename Tin> __device__ __forceinline__ float as_float(Tin x) { return to_f32<Tin>(x); }
-
 // Partial results of a slice: maximum and sum of exponentials below it, then K keys.
 struct SliceHead {
     float max, sum;
 };
 
+// The r-th largest of the warp's 32 values (0: fewer than r are above 0).
+__device__ __forceinline__ uint32_t rth_of_warp(uint32_t x, int r, int lane) {
+    uint32_t m = 0;
+    for (int i = 0; i < r; ++i) {
+        m = __reduce_max_sync(0xffffffffu, x);
+        if (lane == __ffs(__ballot_sync(0xffffffffu, x == m)) - 1) x = 0;
+    }
+    return m;
+}
+
 // The K-th largest of the 256 keys in `best` (all different but for zeros, of which any
 // number may stand for threads without a value), by one warp: each lane holds eight.
-__device__ __forceinline__ unsigned long long kth_of_256(const unsigned long long *best, int K, int lane) {
+__device__ __noinline__ unsigned long long kth_of_256(const unsigned long long *best, int K, int lane) {
     unsigned long long x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = best[lane + 32 * i];
@@ -65,94 +74,122 @@ __device__ __forceinline__ unsigned long long kth_of_256(const unsigned long lon
     return t;
 }
 
-template <typename Tin>
+template <typename Tin, int EACH>
 __global__ void __launch_bounds__(kThreads)
 gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K, int nsl, SliceHead *__restrict__ heads,
                 unsigned long long *__restrict__ keys) {
+    constexpr int kCap = 256;  // values at or above the bound before the fallback
     __shared__ unsigned long long best[kThreads];
-    __shared__ unsigned long long found[kMaxK * kEach];
-    __shared__ float red_m[kThreads / 32], red_s[kThreads / 32];
+    __shared__ unsigned long long found[kMaxK * kEachMost];
+    __shared__ float red_m[kWarps], red_s[kWarps];
+    __shared__ uint32_t red_t[kWarps];
     __shared__ unsigned long long s_bound;
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / nsl;
-    const int sl = (int)(blockIdx.x % nsl), i0 = sl * kSlice;
+    const int i0 = (int)(blockIdx.x % nsl) * (kThreads * EACH);
     const Tin *p = logits + row * row_stride;
     constexpr int kVec = 16 / (int)sizeof(Tin);
     const bool wide = ((uintptr_t)(p + i0) & 15) == 0;
     // logit e of this thread: index i0 + (e / kVec) * 256 kVec + tid * kVec + e % kVec
-    float x[kEach];
+    float x[EACH];
     auto index_of = [&](int e) { return i0 + (e / kVec) * (kThreads * kVec) + tid * kVec + e % kVec; };
 #pragma unroll
-    for (int c = 0; c < kEach / kVec; ++c) {
+    for (int c = 0; c < EACH / kVec; ++c) {
         const int i = index_of(c * kVec);
         if (wide && i + kVec <= V) {
             const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p + i));
             const Tin *t = reinterpret_cast<const Tin *>(&w);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) x[c * kVec + e] = as_float<Tin>(t[e]);
+            for (int e = 0; e < kVec; ++e) x[c * kVec + e] = to_f32<Tin>(t[e]);
         } else {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) x[c * kVec + e] = i + e < V ? as_float<Tin>(p[i + e]) : -INFINITY;
+            for (int e = 0; e < kVec; ++e) x[c * kVec + e] = i + e < V ? to_f32<Tin>(p[i + e]) : -INFINITY;
         }
     }
     if (tid == 0) s_count = 0;
-    // the thread's best (lowest index among equals), its maximum with NaN seen
-    unsigned long long mine = 0;
-    float m = -INFINITY;
-    bool nan = false;
+    // the thread's maximum and its sum of 2^((x - max) log2 e); a NaN makes the sum NaN
+    float m = x[0];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        nan |= x[e] != x[e];
-        m = fmaxf(m, x[e]);
+    for (int e = 1; e < EACH; ++e) m = fmaxf(m, x[e]);
+    // (x - max before the factor: the type's lowest value times log2 e would overflow)
+    const float base = m > -INFINITY ? m : 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < EACH; e += 2) {
+        const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[e], x[e + 1]), make_float2(-base, -base)),
+                                    make_float2(kLog2e, kLog2e));
+        sum += sm100::ex2(y.x);
+        sum += sm100::ex2(y.y);
     }
+    // (a thread behind the vocabulary has nothing, not even -infinity)
+    const uint32_t top = index_of(0) < V ? order_bits(m) : 0u;
+    const uint32_t t = rth_of_warp(top, (K + kWarps - 1) / kWarps, lane);
+    float wm = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+    sum *= m > -INFINITY ? sm100::ex2((m - wm) * kLog2e) : 1.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+        red_m[warp] = wm;
+        red_s[warp] = sum;
+        red_t[warp] = t;
+    }
+    __syncthreads();
+    uint32_t bound = red_t[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) bound = min(bound, red_t[w]);
     auto key_of = [&](int e) {
         const int i = index_of(e);
         return i < V ? ((unsigned long long)order_bits(x[e]) << 32) | (uint32_t)~i : 0ull;
     };
+    if (top >= bound && top > 0) {
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        const unsigned long long kx = key_of(e);
-        mine = kx > mine ? kx : mine;
-    }
-    best[tid] = mine;
-    // maximum of the block, then the sum of 2^((x - max) log2 e)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) red_m[warp] = m;
-    const bool any_nan = __syncthreads_or(nan);
-    m = red_m[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, red_m[w]);
-    float sum = 0.f;
-    if (m > -INFINITY) {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) sum += x[e] > -INFINITY ? exp2f((x[e] - m) * kLog2e) : 0.f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red_s[warp] = sum;
-    if (warp == 0) {
-        const unsigned long long t = kth_of_256(best, K, lane);
-        if (lane == 0) s_bound = t;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        float t = 0.f;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) t += red_s[w];
-        heads[blockIdx.x] = SliceHead{any_nan ? NAN : m, t};
-    }
-    const unsigned long long bound = s_bound > 0 ? s_bound : 1;
-    if (mine >= bound) {  // at most K threads
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const unsigned long long kx = key_of(e);
-            if (kx >= bound) found[atomicAdd(&s_count, 1)] = kx;
+        for (int e = 0; e < EACH; ++e) {
+            if (index_of(e) < V && order_bits(x[e]) >= bound) {
+                const int at = atomicAdd(&s_count, 1);
+                if (at < kCap) found[at] = key_of(e);
+            }
         }
     }
+    if (tid == 0) {
+        float bm = red_m[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, red_m[w]);
+        double all = 0.0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            all += red_m[w] > -INFINITY ? (double)red_s[w] * (double)exp2f((red_m[w] - bm) * kLog2e) : (double)red_s[w];
+        heads[blockIdx.x] = SliceHead{bm, (float)all};
+    }
     __syncthreads();
-    const int n = s_count;
+    int n = s_count;
+    if (n > kCap) {  // (the same for the whole block)
+        unsigned long long mine = 0;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const unsigned long long kx = key_of(e);
+            mine = kx > mine ? kx : mine;
+        }
+        best[tid] = mine;
+        __syncthreads();
+        if (tid == 0) s_count = 0;
+        if (warp == 0) {
+            const unsigned long long k = kth_of_256(best, K, lane);
+            if (lane == 0) s_bound = k > 0 ? k : 1;
+        }
+        __syncthreads();
+        if (mine >= s_bound) {  // at most K threads
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) {
+                const unsigned long long kx = key_of(e);
+                if (kx >= s_bound) found[atomicAdd(&s_count, 1)] = kx;
+            }
+        }
+        __syncthreads();
+        n = s_count;
+    }
     unsigned long long *to = keys + (int64_t)blockIdx.x * K;
     for (int i = tid; i < n; i += kThreads) {
         const unsigned long long kx = found[i];
@@ -163,7 +200,8 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
     for (int i = n + tid; i < K; i += kThreads) to[i] = 0;  // fewer values than K
 }
 
-// Joins the slices of one request.
+// A continuation; none: flat = kNone.
+constexpr int kNone = 0x7fffffff;
 struct Cand {
     double score;
     int flat;
@@ -171,67 +209,102 @@ struct Cand {
         return score > o.score || (score == o.score && flat < o.flat);
     }
 };
+// The upper half of a score's order bits (scores in order have halves in order; > 0).
+__device__ __forceinline__ uint32_t order_half(double x) {
+    const unsigned long long u = (unsigned long long)__double_as_longlong(x == 0.0 ? 0.0 : x);
+    return (uint32_t)((u >> 63 ? ~u : u | (1ull << 63)) >> 32);
+}
 
+// Joins the slices of one request.
 __global__ void __launch_bounds__(kThreads)
 gdn_beam_join(const float *__restrict__ scores, int W, int V, int K, int nsl, const SliceHead *__restrict__ heads,
               const unsigned long long *__restrict__ keys, float *__restrict__ out_scores,
               int32_t *__restrict__ out_parent, int32_t *__restrict__ out_token) {
-    __shared__ double s_add[64];    // a beam's score minus its normaliser (not finite: all its scores are -infinity)
-    __shared__ Cand s_best[kThreads];
+    constexpr int kCap = 512;
+    __shared__ double s_add[64];  // a beam's score minus its normaliser (not finite: all its scores are -infinity)
+    __shared__ Cand s_found[kCap];
+    __shared__ uint32_t red_t[kWarps];
+    __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t b = blockIdx.x;
-    for (int w = warp; w < W; w += kThreads / 32) {
+    if (tid == 0) s_count = 0;
+    for (int w = warp; w < W; w += kWarps) {
         const SliceHead *hd = heads + (b * W + w) * nsl;
         float m = -INFINITY;
-        bool nan = false;
-        for (int i = lane; i < nsl; i += 32) {
-            nan |= hd[i].max != hd[i].max;
-            m = fmaxf(m, hd[i].max);
-        }
-        nan = __any_sync(0xffffffffu, nan);
+        for (int i = lane; i < nsl; i += 32) m = fmaxf(m, hd[i].max);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         double sum = 0.0;
-        for (int i = lane; i < nsl; i += 32)
-            if (hd[i].max > -INFINITY) sum += (double)hd[i].sum * exp((double)hd[i].max - (double)m);
+        for (int i = lane; i < nsl; i += 32) {
+            const SliceHead x = hd[i];  // (a slice of -infinities has the sum 0, one with a NaN has NaN)
+            sum += x.max > -INFINITY ? (double)x.sum * exp((double)x.max - (double)m) : (double)x.sum;
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) {
-            const double add = (scores ? (double)scores[b * W + w] : 0.0) - ((double)m + log(sum));
-            s_add[w] = nan ? (double)NAN : add;
-        }
+        if (lane == 0) s_add[w] = (scores ? (double)scores[b * W + w] : 0.0) - ((double)m + log(sum));
     }
     __syncthreads();
-    const int n = W * nsl * K;
+    const int per = nsl * K, n = W * per;
     const unsigned long long *ks = keys + b * n;
-    // candidates in order, best first: K rounds of the best one below the last
+    // Candidate i: key i, or where a beam's scores are all -infinity its first K tokens.
     auto cand_of = [&](int i) {
-        const int w = i / (nsl * K), r = i - w * nsl * K;
+        const int w = i / per, r = i - w * per;
         const double add = s_add[w];
-        if (!(fabs(add) < INFINITY)) return r < K && r < V ? Cand{-INFINITY, w * V + r} : Cand{-INFINITY, 0x7fffffff};
+        if (!(fabs(add) < INFINITY)) return Cand{-INFINITY, r < K && r < V ? w * V + r : kNone};
         const unsigned long long kx = ks[i];
-        if (kx == 0) return Cand{-INFINITY, 0x7fffffff};
-        return Cand{add + (double)value_of((uint32_t)(kx >> 32)), w * V + (int)~(uint32_t)kx};
+        return kx ? Cand{add + (double)value_of((uint32_t)(kx >> 32)), w * V + (int)~(uint32_t)kx} : Cand{-INFINITY, kNone};
     };
-    Cand last{INFINITY, -1};
-    for (int r = 0; r < K; ++r) {
-        Cand mine{-INFINITY, 0x7fffffff};
+    uint32_t top = 0;
+    for (int i = tid; i < n; i += kThreads) {
+        const Cand c = cand_of(i);
+        if (c.flat != kNone) top = max(top, order_half(c.score));
+    }
+    const uint32_t t = rth_of_warp(top, (K + kWarps - 1) / kWarps, lane);
+    if (lane == 0) red_t[warp] = t;
+    __syncthreads();
+    uint32_t bound = red_t[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) bound = min(bound, red_t[w]);
+    if (top >= bound)
         for (int i = tid; i < n; i += kThreads) {
             const Cand c = cand_of(i);
-            if (c.flat != 0x7fffffff && last.better(c) && c.better(mine)) mine = c;
+            if (c.flat != kNone && order_half(c.score) >= bound) {
+                const int at = atomicAdd(&s_count, 1);
+                if (at < kCap) s_found[at] = c;
+            }
         }
-        s_best[tid] = mine;
+    __syncthreads();
+    const int found = s_count;
+    auto put = [&](int r, const Cand &c) {
+        out_scores[b * K + r] = (float)c.score;
+        out_parent[b * K + r] = c.flat / V;
+        out_token[b * K + r] = c.flat % V;
+    };
+    if (found <= kCap) {  // (the same for the whole block)
+        for (int i = tid; i < found; i += kThreads) {
+            const Cand c = s_found[i];
+            int rank = 0;
+            for (int j = 0; j < found; ++j) rank += s_found[j].better(c);
+            if (rank < K) put(rank, c);
+        }
+        return;
+    }
+    __syncthreads();
+    Cand last{INFINITY, -1};
+    for (int r = 0; r < K; ++r) {  // the best one below the last, K times
+        Cand mine{-INFINITY, kNone};
+        for (int i = tid; i < n; i += kThreads) {
+            const Cand c = cand_of(i);
+            if (c.flat != kNone && last.better(c) && c.better(mine)) mine = c;
+        }
+        s_found[tid] = mine;
         __syncthreads();
         for (int o = kThreads / 2; o > 0; o >>= 1) {
-            if (tid < o && s_best[tid + o].better(s_best[tid])) s_best[tid] = s_best[tid + o];
+            if (tid < o && s_found[tid + o].better(s_found[tid])) s_found[tid] = s_found[tid + o];
             __syncthreads();
         }
-        last = s_best[0];
-        if (tid == 0) {
-            out_scores[b * K + r] = (float)last.score;
-            out_parent[b * K + r] = last.flat / V;
-            out_token[b * K + r] = last.flat % V;
-        }
+        last = s_found[0];
+        if (tid == 0) put(r, last);
         __syncthreads();
     }
 }
@@ -259,7 +332,23 @@ gdn_state_reorder_kernel(uint4 *__restrict__ state, const int32_t *__restrict__ 
         if (w < W && s_parent[w] != w) base[w * cols] = x[w];
 }
 
-int slices(const gdn_beam_desc &d) { return (d.V + kSlice - 1) / kSlice; }
+// Logits of a thread: 32, or 8 where slices of 8192 would leave SMs without one (both measured
+// on 4 beams of 32,000: 16 blocks against 64).
+int each(const gdn_beam_desc &d) {
+    const int64_t big = (int64_t)d.B * d.W * ((d.V + kThreads * kEachMost - 1) / (kThreads * kEachMost));
+    return big >= 148 ? kEachMost : 8;
+}
+int slices(const gdn_beam_desc &d) { return (d.V + kThreads * each(d) - 1) / (kThreads * each(d)); }
+
+template <typename Tin>
+void launch_slices(const gdn_beam_desc &d, const void *logits, int nsl, SliceHead *heads, unsigned long long *keys,
+                   cudaStream_t s) {
+    const unsigned n = (unsigned)(d.B * d.W * nsl);
+    if (each(d) == kEachMost)
+        gdn_beam_slices<Tin, kEachMost><<<n, kThreads, 0, s>>>((const Tin *)logits, d.row_stride, d.V, d.K, nsl, heads, keys);
+    else
+        gdn_beam_slices<Tin, 8><<<n, kThreads, 0, s>>>((const Tin *)logits, d.row_stride, d.V, d.K, nsl, heads, keys);
+}
 
 }  // namespace
 
@@ -272,17 +361,15 @@ gdn_status launch_beam_select(const gdn_beam_desc &d, const void *logits, const 
                               int32_t *out_parent, int32_t *out_token, void *ws, cudaStream_t s) {
     const int nsl = slices(d);
     const int64_t n = d.B * d.W * nsl;
-    if (n > 0x7fffffffLL) return fail(GDN_ERR_UNSUPPORTED, "grid too large");
+    if (n > 0x7fffffffLL || (int64_t)d.W * nsl * d.K > 0x7fffffffLL) return fail(GDN_ERR_UNSUPPORTED, "grid too large");
     SliceHead *heads = static_cast<SliceHead *>(ws);
     auto *keys = reinterpret_cast<unsigned long long *>(static_cast<char *>(ws) + ((size_t)n * sizeof(SliceHead) + 255) / 256 * 256);
     {
         LaunchScope ls("gdn_beam_slices", s);
         if (d.dtype == GDN_BF16)
-            gdn_beam_slices<__nv_bfloat16><<<(unsigned)n, kThreads, 0, s>>>((const __nv_bfloat16 *)logits, d.row_stride,
-                                                                          d.V, d.K, nsl, heads, keys);
+            launch_slices<__nv_bfloat16>(d, logits, nsl, heads, keys, s);
         else
-            gdn_beam_slices<float><<<(unsigned)n, kThreads, 0, s>>>((const float *)logits, d.row_stride, d.V, d.K, nsl,
-                                                                    heads, keys);
+            launch_slices<float>(d, logits, nsl, heads, keys, s);
     }
     gdn_status st = check_launch("gdn_beam_slices");
     if (st != GDN_OK) return st;

@@ -354,49 +354,56 @@ def gdn_state_select(step_states, accept, state, *, stream=None):
 # rotation of queries and keys, beam search over recurrent states
 # ---------------------------------------------------------------------------
 
-class _Launch:
-    """Where a call runs: the device its tensors are on and the stream it is queued on
-    (the current one of that device, or `stream`), also current for what the call allocates."""
+def _where(stream, t, *others):
+    """The (device index, raw stream) of a call: the device its tensors are on and `stream`, or the current
+    stream of that device."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors (the library has no CPU path)")
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"tensors are on different devices: {t.device} and {o.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+    return dev, stream.cuda_stream
 
-    def __init__(self, stream, *ts):
-        ts = [t for t in ts if t is not None]
-        _need_cuda_any(*ts)
-        dev = ts[0].device
-        for t in ts:
-            if t.device != dev:
-                raise ValueError(f"tensors are on different devices: {dev} and {t.device}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-        self.device = dev
-        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
-        self._with = torch.cuda.stream(self.stream)
+
+class _On:
+    """The device of a call made current, and its stream too (so that what is allocated for it belongs to that
+    stream), where they are not."""
+
+    def __init__(self, dev, stream):
+        self._with = None
+        if stream is not None:
+            self._with = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != dev:
+            self._with = torch.cuda.device(dev)
 
     def __enter__(self):
-        self._with.__enter__()  # makes the stream's device current too
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        if self._with is not None:
+            self._with.__enter__()
 
     def __exit__(self, *exc):
-        return self._with.__exit__(*exc)
+        if self._with is not None:
+            self._with.__exit__(*exc)
 
 
-def _need_cuda_any(*ts):
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors (the library has no CPU path)")
-
-
-def _need(name, t, shape, dtype=None, optional=False):
+def _need(name, t, shape, dtype=None):
     """`t` is a contiguous tensor of `shape` (and `dtype`)."""
     if t is None:
-        if optional:
-            return
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def gdn_linattn_workspace_size(B, T, H, dk, dv, num_seqs, *, dtype=torch.bfloat16, hk=0) -> int:
@@ -423,34 +430,41 @@ def gdn_linattn_chunk_fwd(q, k, v, log_gate, initial_state=None, cu_seqlens=None
     _need("v", v, (B, T, H, dv), q.dtype)
     fixed = log_gate.dim() == 1
     _need("log_gate", log_gate, (H,) if fixed else (B, T, H), torch.float32)
-    _need("initial_state", initial_state, (N, H, dv, dk), torch.float32, optional=True)
-    _need("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, optional=True)
-    given = [t for t in (out, final_state, snapshots, workspace) if isinstance(t, torch.Tensor)]
-    with (at := _Launch(stream, q, k, v, log_gate, initial_state, cu_seqlens, *given)) as s:
+    if initial_state is not None:
+        _need("initial_state", initial_state, (N, H, dv, dk), torch.float32)
+    if cu_seqlens is not None:
+        _need("cu_seqlens", cu_seqlens, (N + 1,), torch.int32)
+    if out is not None:
+        _need("out", out, (B, T, H, dv), q.dtype)
+    if isinstance(final_state, torch.Tensor):
+        _need("final_state", final_state, (N, H, dv, dk), torch.float32)
+    if snapshots is not None and snapshot_stride > 0:
+        _need("snapshots", snapshots, (B, T // snapshot_stride, H, dv, dk), torch.float32)
+    given = final_state if isinstance(final_state, torch.Tensor) else None
+    dev, raw = _where(stream, q, k, v, log_gate, initial_state, cu_seqlens, out, given, snapshots, workspace)
+    with _On(dev, stream):
         if out is None:
-            out = torch.empty((B, T, H, dv), dtype=q.dtype, device=at.device)
+            out = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
         if final_state is True:
-            final_state = torch.empty((N, H, dv, dk), dtype=torch.float32, device=at.device)
+            final_state = torch.empty((N, H, dv, dk), dtype=torch.float32, device=q.device)
         elif final_state is False:
             final_state = None
         if snapshot_stride > 0 and snapshots is None:
-            snapshots = torch.empty((B, T // snapshot_stride, H, dv, dk), dtype=torch.float32, device=at.device)
-        _need("out", out, (B, T, H, dv), q.dtype)
-        _need("final_state", final_state, (N, H, dv, dk), torch.float32, optional=True)
-        if snapshot_stride > 0:
-            _need("snapshots", snapshots, (B, T // snapshot_stride, H, dv, dk), torch.float32)
+            snapshots = torch.empty((B, T // snapshot_stride, H, dv, dk), dtype=torch.float32, device=q.device)
         d = make_desc(B, T, H, dk, dv, code, False, scale, Hq)
         d.gate = GDN_GATE_CONST if fixed else GDN_GATE_HEAD
         if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib, lib.gdn_linattn_workspace_size(ctypes.byref(d), int(N), ctypes.byref(n)))
-            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=at.device)
+            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=q.device)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        _check(lib, lib.gdn_linattn_chunk_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate),
-                                              _ptr(initial_state), _ptr(cu_seqlens), int(N), int(snapshot_stride),
-                                              _ptr(out), _ptr(final_state), _ptr(snapshots), _ptr(workspace),
-                                              workspace.numel() * workspace.element_size(), s))
+        st = lib.gdn_linattn_chunk_fwd(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
+                                       _addr(initial_state), _addr(cu_seqlens), N, int(snapshot_stride),
+                                       out.data_ptr(), _addr(final_state), _addr(snapshots), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), raw)
+        if st != GDN_OK:
+            _check(lib, st)
     return out, final_state, snapshots
 
 
@@ -468,15 +482,18 @@ def gdn_linattn_decode_step(q, k, v, log_gate, state, *, scale=1.0, out=None, st
     fixed = log_gate.dim() == 1
     _need("log_gate", log_gate, (H,) if fixed else ((B,) if log_gate.dim() == 2 else (B, 1)) + (H,), torch.float32)
     _need("state", state, (B, H, dv, dk), torch.float32)
-    with (at := _Launch(stream, q, k, v, log_gate, state, out)) as s:
-        if out is None:
-            out = torch.empty((B, 1, H, dv), dtype=q.dtype, device=at.device)
-        if out.numel() != B * H * dv or out.dtype != q.dtype or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous (B, 1, H, dv) tensor of {q.dtype}")
-        d = make_desc(B, 1, H, dk, dv, code, False, scale, hk)
-        d.gate = GDN_GATE_CONST if fixed else GDN_GATE_HEAD
-        _check(lib, lib.gdn_linattn_decode_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate),
-                                                _ptr(state), _ptr(out), s))
+    if out is None:
+        with _On(q.get_device(), stream):
+            out = torch.empty((B, 1, H, dv), dtype=q.dtype, device=q.device)
+    elif out.numel() != B * H * dv or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous (B, 1, H, dv) tensor of {q.dtype}")
+    dev, raw = _where(stream, q, k, v, log_gate, state, out)
+    d = GdnDesc(B, 1, H, dk, dv, code, GDN_GATE_CONST if fixed else GDN_GATE_HEAD, float(scale), hk if hk != H else 0)
+    with _On(dev, None):
+        st = lib.gdn_linattn_decode_step(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
+                                         state.data_ptr(), out.data_ptr(), raw)
+    if st != GDN_OK:
+        _check(lib, st)
     return out
 
 
@@ -513,20 +530,28 @@ def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, *,
     if rot:
         _need("inv_freq", inv_freq, (rot // 2,), torch.float32)
         _need("positions", positions, (B, T), torch.int32)
-    _need("q_weight", q_weight, (dim,), torch.float32, optional=True)
-    _need("k_weight", k_weight, (dim,), torch.float32, optional=True)
-    used = [q, k, positions if rot else None, inv_freq, q_weight, k_weight, q_out, k_out]
-    with (at := _Launch(stream, *used)) as s:
-        if q_out is None:
-            q_out = torch.empty((B, T, hq, dim), dtype=q.dtype, device=at.device)
-        if k_out is None:
-            k_out = torch.empty((B, T, hk, dim), dtype=q.dtype, device=at.device)
+    else:
+        positions = None
+    if q_weight is not None:
+        _need("q_weight", q_weight, (dim,), torch.float32)
+    if k_weight is not None:
+        _need("k_weight", k_weight, (dim,), torch.float32)
+    if q_out is not None:
         _need("q_out", q_out, (B, T, hq, dim), q.dtype)
+    if k_out is not None:
         _need("k_out", k_out, (B, T, hk, dim), q.dtype)
-        d = GdnQkRopeDesc(B * T, hq, hk, dim, rot, 1 if interleaved else 0, code, _token_rows("q", q),
-                          _token_rows("k", k) if hk else 0, float(eps), float(weight_offset))
-        _check(lib, lib.gdn_qk_norm_rope(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(positions if rot else None),
-                                         _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out), s))
+    dev, raw = _where(stream, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    d = GdnQkRopeDesc(B * T, hq, hk, dim, rot, 1 if interleaved else 0, code, _token_rows("q", q),
+                      _token_rows("k", k) if hk else 0, float(eps), float(weight_offset))
+    with _On(dev, stream):
+        if q_out is None:
+            q_out = torch.empty((B, T, hq, dim), dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty((B, T, hk, dim), dtype=q.dtype, device=q.device)
+        st = lib.gdn_qk_norm_rope(ctypes.byref(d), q.data_ptr(), k.data_ptr(), _addr(positions), _addr(inv_freq),
+                                  _addr(q_weight), _addr(k_weight), q_out.data_ptr(), k_out.data_ptr(), raw)
+    if st != GDN_OK:
+        _check(lib, st)
     return q_out, k_out
 
 
@@ -545,25 +570,32 @@ def gdn_beam_select(logits, scores, K, *, out_scores=None, out_parent=None, out_
     if B > 1 and W > 1 and st[0] != W * st[1]:
         raise ValueError("logits: rows must be evenly spaced over (B, W)")
     stride = V if B * W <= 1 else (st[1] if W > 1 else st[0])
-    _need("scores", scores, (B, W), torch.float32, optional=True)
-    with (at := _Launch(stream, logits, scores, out_scores, out_parent, out_token, workspace)) as s:
-        new = lambda dt: torch.empty((B, K), dtype=dt, device=at.device)  # noqa: E731
-        out_scores = new(torch.float32) if out_scores is None else out_scores
-        out_parent = new(torch.int32) if out_parent is None else out_parent
-        out_token = new(torch.int32) if out_token is None else out_token
-        _need("out_scores", out_scores, (B, K), torch.float32)
-        _need("out_parent", out_parent, (B, K), torch.int32)
-        _need("out_token", out_token, (B, K), torch.int32)
-        d = GdnBeamDesc(B, W, V, int(K), code, stride)
+    if scores is not None:
+        _need("scores", scores, (B, W), torch.float32)
+    for name, t, dt in (("out_scores", out_scores, torch.float32), ("out_parent", out_parent, torch.int32),
+                        ("out_token", out_token, torch.int32)):
+        if t is not None:
+            _need(name, t, (B, K), dt)
+    dev, raw = _where(stream, logits, scores, out_scores, out_parent, out_token, workspace)
+    d = GdnBeamDesc(B, W, V, int(K), code, stride)
+    with _On(dev, stream):
+        if out_scores is None:
+            out_scores = torch.empty((B, K), dtype=torch.float32, device=logits.device)
+        if out_parent is None:
+            out_parent = torch.empty((B, K), dtype=torch.int32, device=logits.device)
+        if out_token is None:
+            out_token = torch.empty((B, K), dtype=torch.int32, device=logits.device)
         if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib, lib.gdn_beam_workspace_size(ctypes.byref(d), ctypes.byref(n)))
-            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=at.device)
+            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=logits.device)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        _check(lib, lib.gdn_beam_select(ctypes.byref(d), _ptr(logits), _ptr(scores), _ptr(out_scores),
-                                        _ptr(out_parent), _ptr(out_token), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), s))
+        st = lib.gdn_beam_select(ctypes.byref(d), logits.data_ptr(), _addr(scores), out_scores.data_ptr(),
+                                 out_parent.data_ptr(), out_token.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), raw)
+    if st != GDN_OK:
+        _check(lib, st)
     return out_scores, out_parent, out_token
 
 
@@ -578,8 +610,11 @@ def gdn_state_reorder(state, parent, *, stream=None):
     if state.dim() < 1 or state.shape[0] != B * W or not state.is_contiguous():
         raise ValueError(f"state must be contiguous with {B * W} rows")
     row_bytes = state.numel() // max(B * W, 1) * state.element_size()
-    with _Launch(stream, state, parent) as s:
-        _check(lib, lib.gdn_state_reorder(_ptr(state), _ptr(parent), int(B), int(W), int(row_bytes), s))
+    dev, raw = _where(stream, state, parent)
+    with _On(dev, None):
+        st = lib.gdn_state_reorder(state.data_ptr(), parent.data_ptr(), B, W, row_bytes, raw)
+    if st != GDN_OK:
+        _check(lib, st)
     return state
 
 
