@@ -91,40 +91,59 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
     const Tin *p = logits + row * row_stride;
     constexpr int kVec = 16 / (int)sizeof(Tin);
     const bool wide = ((uintptr_t)(p + i0) & 15) == 0;
-    // logit e of this thread: index i0 + (e / kVec) * 256 kVec + tid * kVec + e % kVec
-    float x[EACH];
+    // logit e of this thread: index i0 + (e / kVec) * 256 kVec + tid * kVec + e % kVec, kept as it
+    // lies in memory (bf16: half the registers, so more blocks per SM)
+    uint4 raw[EACH / kVec];
+    auto x = [&](int e) {
+        const uint4 &w = raw[e / kVec];
+        if (kVec == 4) {
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            return __uint_as_float(u[e % 4]);
+        }
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        return __uint_as_float(e & 1 ? u[(e % 8) / 2] & 0xffff0000u : u[(e % 8) / 2] << 16);
+    };
     auto index_of = [&](int e) { return i0 + (e / kVec) * (kThreads * kVec) + tid * kVec + e % kVec; };
+    constexpr uint32_t kLow = kVec == 4 ? 0xff800000u : 0xff80ff80u;  // -infinity
 #pragma unroll
     for (int c = 0; c < EACH / kVec; ++c) {
         const int i = index_of(c * kVec);
         if (wide && i + kVec <= V) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p + i));
-            const Tin *t = reinterpret_cast<const Tin *>(&w);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) x[c * kVec + e] = to_f32<Tin>(t[e]);
+            raw[c] = __ldcs(reinterpret_cast<const uint4 *>(p + i));
         } else {
+            uint32_t u[4] = {kLow, kLow, kLow, kLow};
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) x[c * kVec + e] = i + e < V ? to_f32<Tin>(p[i + e]) : -INFINITY;
+            for (int e = 0; e < kVec; ++e)
+                if (i + e < V) {
+                    if (kVec == 4)
+                        u[e] = reinterpret_cast<const uint32_t *>(p)[i + e];
+                    else
+                        u[e / 2] = e & 1 ? (u[e / 2] & 0xffffu) | (uint32_t)reinterpret_cast<const uint16_t *>(p)[i + e] << 16
+                                         : (u[e / 2] & 0xffff0000u) | reinterpret_cast<const uint16_t *>(p)[i + e];
+                }
+            raw[c] = make_uint4(u[0], u[1], u[2], u[3]);
         }
     }
     if (tid == 0) s_count = 0;
     // the thread's maximum and its sum of 2^((x - max) log2 e); a NaN makes the sum NaN
-    float m = x[0];
+    float m = x(0);
 #pragma unroll
-    for (int e = 1; e < EACH; ++e) m = fmaxf(m, x[e]);
+    for (int e = 1; e < EACH; ++e) m = fmaxf(m, x(e));
     // (x - max before the factor: the type's lowest value times log2 e would overflow)
     const float base = m > -INFINITY ? m : 0.f;
     float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < EACH; e += 2) {
-        const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[e], x[e + 1]), make_float2(-base, -base)),
+        const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x(e), x(e + 1)), make_float2(-base, -base)),
                                     make_float2(kLog2e, kLog2e));
         sum += sm100::ex2(y.x);
         sum += sm100::ex2(y.y);
     }
     // (a thread behind the vocabulary has nothing, not even -infinity)
     const uint32_t top = index_of(0) < V ? order_bits(m) : 0u;
-    const uint32_t t = rth_of_warp(top, (K + kWarps - 1) / kWarps, lane);
+    // (a last slice may leave whole warps without a logit: the others' share grows)
+    const int left = V - i0, busy = left >= kThreads * kVec ? kWarps : (left + 32 * kVec - 1) / (32 * kVec);
+    const uint32_t t = rth_of_warp(top, (K + busy - 1) / busy, lane);
     float wm = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
@@ -139,19 +158,23 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
     __syncthreads();
     uint32_t bound = red_t[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) bound = min(bound, red_t[w]);
-    auto key_of = [&](int e) {
-        const int i = index_of(e);
-        return i < V ? ((unsigned long long)order_bits(x[e]) << 32) | (uint32_t)~i : 0ull;
-    };
+    for (int w = 1; w < kWarps; ++w)
+        if (w < busy) bound = min(bound, red_t[w]);
+    auto key_at = [&](int i) { return ((unsigned long long)order_bits(to_f32<Tin>(p[i])) << 32) | (uint32_t)~i; };
     if (top >= bound && top > 0) {
+        // which of this thread's logits reach the bound (few threads have any): a bit each, then
+        // those are read once more
+        const float least = bound > 0 ? value_of(bound) : -INFINITY;  // (0: a warp with fewer than its share)
+        uint32_t bits = 0;
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            if (index_of(e) < V && order_bits(x[e]) >= bound) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kCap) found[at] = key_of(e);
-            }
-        }
+        for (int e = 0; e < EACH; ++e) bits |= x(e) >= least ? 1u << e : 0u;
+        if (left < kThreads * EACH)
+#pragma unroll
+            for (int e = 0; e < EACH; ++e)
+                if (index_of(e) >= V) bits &= ~(1u << e);
+        int at = atomicAdd(&s_count, __popc(bits));
+        for (; bits; bits &= bits - 1, ++at)
+            if (at < kCap) found[at] = key_at(index_of(__ffs(bits) - 1));
     }
     if (tid == 0) {
         float bm = red_m[0];
@@ -165,11 +188,12 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
     }
     __syncthreads();
     int n = s_count;
-    if (n > kCap) {  // (the same for the whole block)
+    if (n > kCap) {  // (the same for the whole block; the logits are read again)
         unsigned long long mine = 0;
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < EACH; ++e) {
-            const unsigned long long kx = key_of(e);
+            const int i = index_of(e);
+            const unsigned long long kx = i < V ? key_at(i) : 0ull;
             mine = kx > mine ? kx : mine;
         }
         best[tid] = mine;
@@ -181,9 +205,10 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
         }
         __syncthreads();
         if (mine >= s_bound) {  // at most K threads
-#pragma unroll
+#pragma unroll 1
             for (int e = 0; e < EACH; ++e) {
-                const unsigned long long kx = key_of(e);
+                const int i = index_of(e);
+                const unsigned long long kx = i < V ? key_at(i) : 0ull;
                 if (kx >= s_bound) found[atomicAdd(&s_count, 1)] = kx;
             }
         }
@@ -209,21 +234,27 @@ struct Cand {
         return score > o.score || (score == o.score && flat < o.flat);
     }
 };
-// The upper half of a score's order bits (scores in order have halves in order; > 0).
-__device__ __forceinline__ uint32_t order_half(double x) {
+// A score's order bits, of which more is better, as those of a float above.
+__device__ __forceinline__ unsigned long long order_bits(double x) {
     const unsigned long long u = (unsigned long long)__double_as_longlong(x == 0.0 ? 0.0 : x);
-    return (uint32_t)((u >> 63 ? ~u : u | (1ull << 63)) >> 32);
+    return u >> 63 ? ~u : u | (1ull << 63);
 }
 
-// Joins the slices of one request.
+// Joins the slices of one request.  A beam's candidates belong to `lanes` threads.  They are
+// sifted in fp32 (the multiprocessor's 64-bit units would take most of the kernel's time):
+// with |error| <= err, at least K scores are `bound` - err or more, so the K best are among
+// those whose fp32 value is bound - 2 err or more.
 __global__ void __launch_bounds__(kThreads)
-gdn_beam_join(const float *__restrict__ scores, int W, int V, int K, int nsl, const SliceHead *__restrict__ heads,
+gdn_beam_join(const float *__restrict__ scores, int W, int V, int K, int nsl, int lanes, const SliceHead *__restrict__ heads,
               const unsigned long long *__restrict__ keys, float *__restrict__ out_scores,
               int32_t *__restrict__ out_parent, int32_t *__restrict__ out_token) {
     constexpr int kCap = 512;
     __shared__ double s_add[64];  // a beam's score minus its normaliser (not finite: all its scores are -infinity)
-    __shared__ Cand s_found[kCap];
+    __shared__ unsigned long long s_key[kCap];
+    __shared__ int s_flat[kCap];
+    __shared__ Cand s_best[kThreads];
     __shared__ uint32_t red_t[kWarps];
+    __shared__ float red_a[kWarps];
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t b = blockIdx.x;
@@ -246,65 +277,117 @@ gdn_beam_join(const float *__restrict__ scores, int W, int V, int K, int nsl, co
     __syncthreads();
     const int per = nsl * K, n = W * per;
     const unsigned long long *ks = keys + b * n;
-    // Candidate i: key i, or where a beam's scores are all -infinity its first K tokens.
-    auto cand_of = [&](int i) {
-        const int w = i / per, r = i - w * per;
-        const double add = s_add[w];
-        if (!(fabs(add) < INFINITY)) return Cand{-INFINITY, r < K && r < V ? w * V + r : kNone};
-        const unsigned long long kx = ks[i];
-        return kx ? Cand{add + (double)value_of((uint32_t)(kx >> 32)), w * V + (int)~(uint32_t)kx} : Cand{-INFINITY, kNone};
+    // (neighbouring threads have different beams: a warp's best are then a sample of all)
+    const int w = tid % (kThreads / lanes), l = tid / (kThreads / lanes);
+    const double add = w < W ? s_add[w] : 0.0;
+    const float add32 = (float)add;
+    const bool dead = !(fabs(add) < INFINITY);
+    const unsigned long long *mine = ks + (int64_t)w * per;
+    // fp32 value of candidate r of this beam; of a beam whose scores are all -infinity the
+    // candidates are its first K tokens
+    auto approx = [&](int r, bool &any) {
+        if (dead) {
+            any = r < K && r < V;
+            return -INFINITY;
+        }
+        const unsigned long long kx = mine[r];
+        any = kx != 0;
+        return add32 + value_of((uint32_t)(kx >> 32));
     };
+    // turn k takes candidates k lanes .. + lanes - 1, shifted from turn to turn: each slice's keys
+    // are sorted, and a thread should not meet the same places only
+    const int turns = (per + lanes - 1) / lanes;
+    auto place = [&](int k) { return k * lanes + ((l + 5 * k) & (lanes - 1)); };
     uint32_t top = 0;
-    for (int i = tid; i < n; i += kThreads) {
-        const Cand c = cand_of(i);
-        if (c.flat != kNone) top = max(top, order_half(c.score));
+    if (w < W) {
+#pragma unroll 4
+        for (int k = 0; k < turns; ++k) {
+            const int r = place(k);
+            if (r >= per) continue;
+            bool any;
+            const float x = approx(r, any);
+            if (any) top = max(top, order_bits(x));
+        }
     }
     const uint32_t t = rth_of_warp(top, (K + kWarps - 1) / kWarps, lane);
-    if (lane == 0) red_t[warp] = t;
-    __syncthreads();
-    uint32_t bound = red_t[0];
+    float most = w < W && !dead ? fabsf(add32) : 0.f;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) bound = min(bound, red_t[w]);
-    if (top >= bound)
-        for (int i = tid; i < n; i += kThreads) {
-            const Cand c = cand_of(i);
-            if (c.flat != kNone && order_half(c.score) >= bound) {
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) {
+        red_t[warp] = t;
+        red_a[warp] = most;
+    }
+    __syncthreads();
+    uint32_t bits = red_t[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) {
+        bits = min(bits, red_t[i]);
+        most = fmaxf(most, red_a[i]);
+    }
+    most = fmaxf(most, red_a[0]);
+    // (0: a warp with fewer candidates than its share: all of them are wanted)
+    const float bound = bits > 0 ? value_of(bits) : -INFINITY;
+    const float least = bound > -INFINITY ? bound - 4.8e-7f * (most + fabsf(bound)) : bound;  // 2 err, err <= 2^-22 of the terms
+    if (w < W) {
+#pragma unroll 4
+        for (int k = 0; k < turns; ++k) {
+            const int r = place(k);
+            if (r >= per) continue;
+            bool any;
+            const float x = approx(r, any);
+            if (any && x >= least) {
                 const int at = atomicAdd(&s_count, 1);
-                if (at < kCap) s_found[at] = c;
+                if (at < kCap) {
+                    const unsigned long long kx = dead ? 0ull : mine[r];
+                    s_key[at] = order_bits(dead ? -(double)INFINITY : add + (double)value_of((uint32_t)(kx >> 32)));
+                    s_flat[at] = w * V + (dead ? r : (int)~(uint32_t)kx);
+                }
             }
         }
+    }
     __syncthreads();
     const int found = s_count;
-    auto put = [&](int r, const Cand &c) {
-        out_scores[b * K + r] = (float)c.score;
-        out_parent[b * K + r] = c.flat / V;
-        out_token[b * K + r] = c.flat % V;
+    auto put = [&](int r, double score, int flat) {
+        out_scores[b * K + r] = (float)score;
+        out_parent[b * K + r] = flat / V;
+        out_token[b * K + r] = flat % V;
     };
     if (found <= kCap) {  // (the same for the whole block)
         for (int i = tid; i < found; i += kThreads) {
-            const Cand c = s_found[i];
+            const unsigned long long key = s_key[i];
+            const int flat = s_flat[i];
             int rank = 0;
-            for (int j = 0; j < found; ++j) rank += s_found[j].better(c);
-            if (rank < K) put(rank, c);
+#pragma unroll 4
+            for (int j = 0; j < found; ++j) rank += s_key[j] > key || (s_key[j] == key && s_flat[j] < flat);
+            if (rank < K) {
+                const unsigned long long u = key >> 63 ? key ^ (1ull << 63) : ~key;
+                put(rank, __longlong_as_double((long long)u), flat);
+            }
         }
         return;
     }
-    __syncthreads();
+    auto cand_of = [&](int i) {
+        const int v = i / per, r = i - v * per;
+        const double s = s_add[v];
+        if (!(fabs(s) < INFINITY)) return Cand{-INFINITY, r < K && r < V ? v * V + r : kNone};
+        const unsigned long long kx = ks[i];
+        return kx ? Cand{s + (double)value_of((uint32_t)(kx >> 32)), v * V + (int)~(uint32_t)kx} : Cand{-INFINITY, kNone};
+    };
     Cand last{INFINITY, -1};
     for (int r = 0; r < K; ++r) {  // the best one below the last, K times
-        Cand mine{-INFINITY, kNone};
+        Cand c0{-INFINITY, kNone};
         for (int i = tid; i < n; i += kThreads) {
             const Cand c = cand_of(i);
-            if (c.flat != kNone && last.better(c) && c.better(mine)) mine = c;
+            if (c.flat != kNone && last.better(c) && c.better(c0)) c0 = c;
         }
-        s_found[tid] = mine;
+        s_best[tid] = c0;
         __syncthreads();
         for (int o = kThreads / 2; o > 0; o >>= 1) {
-            if (tid < o && s_found[tid + o].better(s_found[tid])) s_found[tid] = s_found[tid + o];
+            if (tid < o && s_best[tid + o].better(s_best[tid])) s_best[tid] = s_best[tid + o];
             __syncthreads();
         }
-        last = s_found[0];
-        if (tid == 0) put(r, last);
+        last = s_best[0];
+        if (tid == 0) put(r, last.score, last.flat);
         __syncthreads();
     }
 }
@@ -375,8 +458,10 @@ gdn_status launch_beam_select(const gdn_beam_desc &d, const void *logits, const 
     if (st != GDN_OK) return st;
     {
         LaunchScope ls("gdn_beam_join", s);
-        gdn_beam_join<<<(unsigned)d.B, kThreads, 0, s>>>(scores, d.W, d.V, d.K, nsl, heads, keys, out_scores, out_parent,
-                                                        out_token);
+        int lanes = kThreads;
+        while (lanes * d.W > kThreads) lanes /= 2;
+        gdn_beam_join<<<(unsigned)d.B, kThreads, 0, s>>>(scores, d.W, d.V, d.K, nsl, lanes, heads, keys, out_scores,
+                                                        out_parent, out_token);
     }
     return check_launch("gdn_beam_join");
 }

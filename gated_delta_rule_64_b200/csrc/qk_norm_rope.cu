@@ -61,7 +61,7 @@ struct RopeArgs {
     float eps, offset;
 };
 
-template <int D, typename Tin>
+template <int D, typename Tin, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) gdn_qk_norm_rope_kernel(const RopeArgs a) {
     constexpr int kGroup = D / 8;               // lanes of a head
     constexpr int kGroups = kThreads / kGroup;  // of a block; as many tokens at most
@@ -69,86 +69,100 @@ __global__ void __launch_bounds__(kThreads, 4) gdn_qk_norm_rope_kernel(const Rop
     const int tid = threadIdx.x, sub = tid % kGroup, group = tid / kGroup;
     const int64_t row0 = (int64_t)blockIdx.x * a.tokens;
     const int tokens = (int)(a.rows - row0 < a.tokens ? a.rows - row0 : a.tokens);
-    const int heads = a.hq + a.hk, half = a.rot / 2;
+    const int half = a.rot / 2;
     // this lane's quads: channels c0 .. c0 + 3 and c1 .. c1 + 3
-    const bool partners = !a.interleaved && 4 * sub < half;
-    const int c0 = partners ? 4 * sub : (a.interleaved ? 8 * sub : a.rot + 8 * (sub - half / 4));
+    const bool partners = !INTER && 4 * sub < half;
+    const int c0 = INTER ? 8 * sub : (partners ? 4 * sub : a.rot + 8 * (sub - half / 4));
     const int c1 = partners ? c0 + half : c0 + 4;
     // this group's token and heads: h0, h0 + step, ...
     const int step = kGroups / a.tokens, t = group / step, h0 = group % step;
     const bool live = t < tokens;
     const int64_t row = row0 + (live ? t : 0);
-    const Tin *q = static_cast<const Tin *>(a.q) + row * a.q_stride, *k = static_cast<const Tin *>(a.k) + row * a.k_stride;
-    Tin *qo = static_cast<Tin *>(a.q_out) + row * a.hq * D, *ko = static_cast<Tin *>(a.k_out) + row * a.hk * D;
 
     typedef typename Raw<Tin>::type raw;
+    const int64_t qo = (int64_t)h0 * D;
+    const Tin *q = static_cast<const Tin *>(a.q) + row * a.q_stride + qo, *k = static_cast<const Tin *>(a.k) + row * a.k_stride + qo;
+    const int nq = live && h0 < a.hq ? (a.hq - h0 + step - 1) / step : 0, nk = live && h0 < a.hk ? (a.hk - h0 + step - 1) / step : 0;
     raw x0 = {}, x1 = {}, y0 = {}, y1 = {};
-    auto load = [&](int h, raw &lo, raw &hi) {
-        if (live && h < heads) {
-            const Tin *p = h < a.hq ? q + h * D : k + (h - a.hq) * D;
-            lo = load_quad(p + c0);
-            hi = load_quad(p + c1);
-        }
-    };
-    load(h0, x0, x1);  // in flight while the angles are formed
-    load(h0 + step, y0, y1);
+    if (nq > 0) {  // in flight while the angles are formed
+        x0 = load_quad(q + c0);
+        x1 = load_quad(q + c1);
+    }
+    if (nq > 1) {
+        y0 = load_quad(q + step * D + c0);
+        y1 = load_quad(q + step * D + c1);
+    }
     for (int i = tid; i < tokens * half; i += kThreads) {
         const double turn = (double)a.pos[row0 + i / half] * (double)a.inv_freq[i % half] * 0.15915494309189533577;
         sincospif((float)(2.0 * (turn - rint(turn))), &s_sin[i], &s_cos[i]);
+    }
+    __syncthreads();
+    Quad cs = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    if (live && (INTER ? c0 < a.rot : partners)) {  // (interleaved: the lane's four pairs in order)
+        const int i = t * half + (INTER ? c0 / 2 : c0);
+        cs = unpack(*reinterpret_cast<const uint4 *>(s_cos + i));
+        sn = unpack(*reinterpret_cast<const uint4 *>(s_sin + i));
     }
     auto weight = [&](const float *w, int c) {
         return w ? Quad{make_float2(a.offset + w[c], a.offset + w[c + 1]), make_float2(a.offset + w[c + 2], a.offset + w[c + 3])}
                  : Quad{make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
     };
-    Quad w0 = weight(a.qw, c0), w1 = weight(a.qw, c1);
-    __syncthreads();
-    Quad cos4 = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sin4 = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    // (interleaved: the lane's four angles belong to its channel pairs in order)
-    const bool turns = live && (a.interleaved ? c0 < a.rot : partners);
-    if (turns) {
-        const int i = t * half + (a.interleaved ? c0 / 2 : c0);
-        cos4 = unpack(*reinterpret_cast<const uint4 *>(s_cos + i));
-        sin4 = unpack(*reinterpret_cast<const uint4 *>(s_sin + i));
-    }
-    bool keys = false;  // the weights are the keys'
-    // every lane of a warp goes round equally often (the shuffles are warp-wide)
-    for (int h = h0, n = (heads + step - 1) / step; n > 0; --n, h += step) {
-        const raw r0 = x0, r1 = x1;
-        x0 = y0;
-        x1 = y1;
-        load(h + 2 * step, y0, y1);
-        Quad p = unpack(r0), r = unpack(r1);
-        float2 s2 = mul2(p.a, p.a);
-        s2 = fma2(p.b, p.b, s2);
-        s2 = fma2(r.a, r.a, s2);
-        s2 = fma2(r.b, r.b, s2);
-        float ss = s2.x + s2.y;
-#pragma unroll
-        for (int o = kGroup / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rs = rsqrtf(ss * (1.f / D) + a.eps);
-        if (!live || h >= heads) continue;
-        if (h >= a.hq && !keys) {
-            keys = true;
-            w0 = weight(a.kw, c0);
-            w1 = weight(a.kw, c1);
-        }
-        const Quad rs4 = {make_float2(rs, rs), make_float2(rs, rs)};
-        p = scale(scale(p, rs4), w0);
-        r = scale(scale(r, rs4), w1);
-        if (turns) {
-            if (partners) {
-                const Quad ps = scale(p, sin4), rsn = scale(r, Quad{make_float2(-sin4.a.x, -sin4.a.y), make_float2(-sin4.b.x, -sin4.b.y)});
-                p = {fma2(p.a, cos4.a, rsn.a), fma2(p.b, cos4.b, rsn.b)};
-                r = {fma2(r.a, cos4.a, ps.a), fma2(r.b, cos4.b, ps.b)};
-            } else {
-                auto turn = [](float2 x, float c, float s) { return make_float2(x.x * c - x.y * s, x.y * c + x.x * s); };
-                p = {turn(p.a, cos4.a.x, sin4.a.x), turn(p.b, cos4.a.y, sin4.a.y)};
-                r = {turn(r.a, cos4.b.x, sin4.b.x), turn(r.b, cos4.b.y, sin4.b.y)};
+    // `n` heads of this group, of `most` that any group of the warp has (the shuffles are warp-wide);
+    // x and y hold the first two.  With the weights taken into the angles (w cos, w sin) a pair of
+    // partners is two multiply-adds each, and the norm one product at the end.
+    auto run = [&](const Tin *src, Tin *dst, int n, int most, const float *wp) {
+        const Quad w0 = weight(wp, c0), w1 = weight(wp, c1);
+        const Quad cp = scale(w0, cs), cr = scale(w1, cs), sp = scale(w0, sn);
+        const Quad sr = {make_float2(-w1.a.x * sn.a.x, -w1.a.y * sn.a.y), make_float2(-w1.b.x * sn.b.x, -w1.b.y * sn.b.y)};
+        const Tin *ahead = src + 2 * step * D;
+        for (int i = 0; i < most; ++i) {
+            const Quad p = unpack(x0), r = unpack(x1);
+            x0 = y0;
+            x1 = y1;
+            if (i + 2 < n) {
+                y0 = load_quad(ahead + c0);
+                y1 = load_quad(ahead + c1);
             }
+            ahead += step * D;
+            float2 s2 = mul2(p.a, p.a);
+            s2 = fma2(p.b, p.b, s2);
+            s2 = fma2(r.a, r.a, s2);
+            s2 = fma2(r.b, r.b, s2);
+            float ss = s2.x + s2.y;
+#pragma unroll
+            for (int o = kGroup / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float f = rsqrtf(ss * (1.f / D) + a.eps);
+            const float2 ff = make_float2(f, f);
+            Quad u, v;
+            if (INTER) {
+                auto turn = [](float2 x, float2 w, float c, float s) {
+                    const float lo = x.x * w.x, hi = x.y * w.y;
+                    return make_float2(lo * c - hi * s, hi * c + lo * s);
+                };
+                u = {turn(p.a, w0.a, cs.a.x, sn.a.x), turn(p.b, w0.b, cs.a.y, sn.a.y)};
+                v = {turn(r.a, w1.a, cs.b.x, sn.b.x), turn(r.b, w1.b, cs.b.y, sn.b.y)};
+            } else {
+                u = {fma2(p.a, cp.a, mul2(r.a, sr.a)), fma2(p.b, cp.b, mul2(r.b, sr.b))};
+                v = {fma2(r.a, cr.a, mul2(p.a, sp.a)), fma2(r.b, cr.b, mul2(p.b, sp.b))};
+            }
+            if (i < n) {
+                store_quad(dst + c0, Quad{mul2(u.a, ff), mul2(u.b, ff)});
+                store_quad(dst + c1, Quad{mul2(v.a, ff), mul2(v.b, ff)});
+            }
+            dst += step * D;
         }
-        Tin *o = h < a.hq ? qo + h * D : ko + (h - a.hq) * D;
-        store_quad(o + c0, p);
-        store_quad(o + c1, r);
+    };
+    run(q, static_cast<Tin *>(a.q_out) + row * a.hq * D + qo, nq, (a.hq + step - 1) / step, a.qw);
+    if (a.hk > 0) {
+        if (nk > 0) {
+            x0 = load_quad(k + c0);
+            x1 = load_quad(k + c1);
+        }
+        if (nk > 1) {
+            y0 = load_quad(k + step * D + c0);
+            y1 = load_quad(k + step * D + c1);
+        }
+        run(k, static_cast<Tin *>(a.k_out) + row * a.hk * D + qo, nk, (a.hk + step - 1) / step, a.kw);
     }
 }
 
@@ -163,10 +177,11 @@ gdn_status launch_d(const gdn_qk_rope_desc &d, RopeArgs &a, cudaStream_t s) {
     a.tokens = tokens;
     const unsigned grid = (unsigned)((d.rows + tokens - 1) / tokens);
     LaunchScope ls("gdn_qk_norm_rope_kernel", s);
-    if (d.dtype == GDN_BF16)
-        gdn_qk_norm_rope_kernel<D, __nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
-    else
-        gdn_qk_norm_rope_kernel<D, float><<<grid, kThreads, 0, s>>>(a);
+    auto kern = d.dtype == GDN_BF16 ? (a.interleaved ? gdn_qk_norm_rope_kernel<D, __nv_bfloat16, true>
+                                                     : gdn_qk_norm_rope_kernel<D, __nv_bfloat16, false>)
+                                    : (a.interleaved ? gdn_qk_norm_rope_kernel<D, float, true>
+                                                     : gdn_qk_norm_rope_kernel<D, float, false>);
+    kern<<<grid, kThreads, 0, s>>>(a);
     return check_launch("gdn_qk_norm_rope_kernel");
 }
 
