@@ -126,19 +126,28 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
     }
     if (tid == 0) s_count = 0;
     // the thread's maximum and its sum of 2^((x - max) log2 e); a NaN makes the sum NaN
-    float m = x(0);
+    float m;
+    if (kVec == 4) {
+        m = x(0);
 #pragma unroll
-    for (int e = 1; e < EACH; ++e) m = fmaxf(m, x(e));
+        for (int e = 1; e < EACH; ++e) m = fmaxf(m, x(e));
+    } else {  // two at a time
+        const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(raw);
+        __nv_bfloat162 m2 = y[0];
+#pragma unroll
+        for (int e = 1; e < EACH / 2; ++e) m2 = __hmax2(m2, y[e]);
+        m = fmaxf(__low2float(m2), __high2float(m2));
+    }
     // (x - max before the factor: the type's lowest value times log2 e would overflow)
     const float base = m > -INFINITY ? m : 0.f;
-    float sum = 0.f;
+    float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < EACH; e += 2) {
         const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x(e), x(e + 1)), make_float2(-base, -base)),
                                     make_float2(kLog2e, kLog2e));
-        sum += sm100::ex2(y.x);
-        sum += sm100::ex2(y.y);
+        sum2 = __fadd2_rn(sum2, make_float2(sm100::ex2(y.x), sm100::ex2(y.y)));
     }
+    float sum = sum2.x + sum2.y;
     // (a thread behind the vocabulary has nothing, not even -infinity)
     const uint32_t top = index_of(0) < V ? order_bits(m) : 0u;
     // (a last slice may leave whole warps without a logit: the others' share grows)
@@ -165,26 +174,37 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
         // which of this thread's logits reach the bound (few threads have any): a bit each, then
         // those are read once more
         const float least = bound > 0 ? value_of(bound) : -INFINITY;  // (0: a warp with fewer than its share)
-        uint32_t bits = 0;
+        uint32_t bits = 0;  // fp32: bit e for logit e; bf16: bit e for logit 2 e, bit 16 + e for 2 e + 1
+        auto logit_of = [](int bit) { return kVec == 4 ? bit : 2 * (bit & 15) + (bit >> 4); };
+        if (kVec == 4) {
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) bits |= x(e) >= least ? 1u << e : 0u;
+            for (int e = 0; e < EACH; ++e) bits |= x(e) >= least ? 1u << e : 0u;
+        } else {  // (the bound is one of the values: exact in bf16)
+            const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(raw);
+            const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
+#pragma unroll
+            for (int e = 0; e < EACH / 2; ++e) bits |= __hge2_mask(y[e], l2) & (0x00010001u << e);
+        }
         if (left < kThreads * EACH)
-#pragma unroll
-            for (int e = 0; e < EACH; ++e)
-                if (index_of(e) >= V) bits &= ~(1u << e);
+            for (uint32_t rest = bits; rest; rest &= rest - 1) {
+                const int bit = __ffs(rest) - 1;
+                if (index_of(logit_of(bit)) >= V) bits &= ~(1u << bit);
+            }
         int at = atomicAdd(&s_count, __popc(bits));
         for (; bits; bits &= bits - 1, ++at)
-            if (at < kCap) found[at] = key_at(index_of(__ffs(bits) - 1));
+            if (at < kCap) found[at] = key_at(index_of(logit_of(__ffs(bits) - 1)));
     }
-    if (tid == 0) {
-        float bm = red_m[0];
+    if (warp == kWarps - 1) {  // the slice's maximum and sum, a warp's part per lane
+        const float wm8 = lane < kWarps ? red_m[lane] : -INFINITY;
+        float bm = wm8;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, red_m[w]);
+        for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
         double all = 0.0;
+        if (lane < kWarps)
+            all = wm8 > -INFINITY ? (double)red_s[lane] * (double)exp2f((wm8 - bm) * kLog2e) : (double)red_s[lane];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            all += red_m[w] > -INFINITY ? (double)red_s[w] * (double)exp2f((red_m[w] - bm) * kLog2e) : (double)red_s[w];
-        heads[blockIdx.x] = SliceHead{bm, (float)all};
+        for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        if (lane == 0) heads[blockIdx.x] = SliceHead{bm, (float)all};
     }
     __syncthreads();
     int n = s_count;

@@ -44,27 +44,46 @@ __device__ __forceinline__ void warp_scans(float x, int lane, Sum &prefix, float
     after = lane < 31 ? s : 0.f;
 }
 
-__device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float c) {
-    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+// Two partial sums of a dot product, four more values (two multiply-adds an instruction).
+__device__ __forceinline__ void dot4(const float4 &a, const float4 &b, float2 &c) {
+    c = __ffma2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y), c);
+    c = __ffma2_rn(make_float2(a.z, a.w), make_float2(b.z, b.w), c);
 }
 
-// Four consecutive values as fp32 (16-byte aligned fp32, 8-byte aligned bf16).
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+// Four consecutive values: as they lie in memory (16-byte aligned fp32, 8-byte aligned bf16), as fp32.
+template <typename Tin> struct Raw4;
+template <> struct Raw4<float> { typedef float4 type; };
+template <> struct Raw4<__nv_bfloat16> { typedef uint2 type; };
+__device__ __forceinline__ float4 widen(const float4 &x) { return x; }
+__device__ __forceinline__ float4 widen(const uint2 &w) {
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                        __uint_as_float(w.y & 0xffff0000u));
 }
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// `n` rows of W values (rows >= len: zeros, not read), `ld` elements apart, into shared rows of LD floats.
+// A chunk's rows of W values, this thread's share: read ahead into registers, then put into
+// shared rows of LD floats.  Rows from len on are zeros, and not read.
 template <int W, int LD, typename Tin>
-__device__ __forceinline__ void stage_rows(float *dst, const Tin *src, int64_t ld, int len) {
-    for (int e = threadIdx.x; e < kC * (W / 4); e += kThreads) {
-        const int r = e / (W / 4), c = e % (W / 4) * 4;
-        const float4 x = r < len ? load4(src + r * ld + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4 *>(dst + r * LD + c) = x;
+struct Rows {
+    static constexpr int N = kC * (W / 4) / kThreads;
+    static_assert(N * kThreads == kC * (W / 4), "whole pieces");
+    typename Raw4<Tin>::type x[N];
+    __device__ __forceinline__ void read(const Tin *src, int64_t ld, int64_t len) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = threadIdx.x + i * kThreads, r = e / (W / 4), c = e % (W / 4) * 4;
+            x[i] = {};
+            if (r < len) x[i] = *reinterpret_cast<const typename Raw4<Tin>::type *>(src + r * ld + c);
+        }
     }
-}
+    __device__ __forceinline__ void put(float *dst) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = threadIdx.x + i * kThreads, r = e / (W / 4), c = e % (W / 4) * 4;
+            *reinterpret_cast<float4 *>(dst + r * LD + c) = widen(x[i]);
+        }
+    }
+};
 
 template <int DK>
 struct Smem {
@@ -105,14 +124,25 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
         *reinterpret_cast<float4 *>(sm.S + (sr + i) * LK + sc) =
             from ? load4(from + (int64_t)(r0 + sr + i) * DK + sc) : make_float4(0.f, 0.f, 0.f, 0.f);
 
+    Rows<DK, LK, Tin> qn, kn;  // the next chunk's, on their way while the current one is worked on
+    Rows<kRows, LV, Tin> vn;
+    float gn = 0.f;
+    auto ahead = [&](int64_t t0) {
+        qn.read(q + t0 * ldk, ldk, s.len - t0);
+        kn.read(k + t0 * ldk, ldk, s.len - t0);
+        vn.read(v + t0 * ldv, ldv, s.len - t0);
+        gn = warp == 0 && t0 + lane < s.len ? gate2(a, fixed, s.start + t0 + lane, h) : 0.f;
+    };
+    if (s.len > 0) ahead(0);
     for (int64_t t0 = 0; t0 < s.len; t0 += kC) {
         const int L = (int)(s.len - t0 < kC ? s.len - t0 : kC);
         __syncthreads();  // the previous chunk is done with the tiles
-        stage_rows<DK, LK>(sm.q, q + t0 * ldk, ldk, L);
-        stage_rows<DK, LK>(sm.k, k + t0 * ldk, ldk, L);
-        stage_rows<kRows, LV>(sm.v, v + t0 * ldv, ldv, L);
+        qn.put(sm.q);
+        kn.put(sm.k);
+        vn.put(sm.v);
+        const float g = gn;
+        if (t0 + kC < s.len) ahead(t0 + kC);
         if (warp == 0) {
-            const float g = lane < L ? gate2(a, fixed, s.start + t0 + lane, h) : 0.f;
             double G;
             float after;
             warp_scans(g, lane, G, after);
@@ -126,53 +156,51 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
         // scores: this thread's tokens i = ti, ti + 16 against j = tj, tj + 16
         const int tj = lane & 15, ti = warp * 2 + (lane >> 4);
         {
-            float acc[2][2] = {};
+            float2 acc[2][2] = {};
 #pragma unroll 8
             for (int c = 0; c < DK; c += 4) {
-                const float4 q0 = *reinterpret_cast<const float4 *>(sm.q + ti * LK + c);
-                const float4 q1 = *reinterpret_cast<const float4 *>(sm.q + (ti + 16) * LK + c);
-                const float4 k0 = *reinterpret_cast<const float4 *>(sm.k + tj * LK + c);
-                const float4 k1 = *reinterpret_cast<const float4 *>(sm.k + (tj + 16) * LK + c);
-                acc[0][0] = dot4(q0, k0, acc[0][0]);
-                acc[0][1] = dot4(q0, k1, acc[0][1]);
-                acc[1][0] = dot4(q1, k0, acc[1][0]);
-                acc[1][1] = dot4(q1, k1, acc[1][1]);
+                const float4 q0 = load4(sm.q + ti * LK + c), q1 = load4(sm.q + (ti + 16) * LK + c);
+                const float4 k0 = load4(sm.k + tj * LK + c), k1 = load4(sm.k + (tj + 16) * LK + c);
+                dot4(q0, k0, acc[0][0]);
+                dot4(q0, k1, acc[0][1]);
+                dot4(q1, k0, acc[1][0]);
+                dot4(q1, k1, acc[1][1]);
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int i = ti + 16 * x, j = tj + 16 * y;
-                    sm.P[i * LP + j] = j <= i ? a.scale * ex2((float)(sm.G[i] - sm.G[j])) * acc[x][y] : 0.f;
+                    sm.P[i * LP + j] = j <= i ? a.scale * ex2((float)(sm.G[i] - sm.G[j])) * (acc[x][y].x + acc[x][y].y) : 0.f;
                 }
         }
         __syncthreads();
         // outputs: tokens ti, ti + 16, channels tj, tj + 16
         {
-            float acc[2][2] = {};
+            float2 part[2][2] = {};
 #pragma unroll 8
             for (int c = 0; c < DK; c += 4) {
-                const float4 q0 = *reinterpret_cast<const float4 *>(sm.q + ti * LK + c);
-                const float4 q1 = *reinterpret_cast<const float4 *>(sm.q + (ti + 16) * LK + c);
-                const float4 s0 = *reinterpret_cast<const float4 *>(sm.S + tj * LK + c);
-                const float4 s1 = *reinterpret_cast<const float4 *>(sm.S + (tj + 16) * LK + c);
-                acc[0][0] = dot4(q0, s0, acc[0][0]);
-                acc[0][1] = dot4(q0, s1, acc[0][1]);
-                acc[1][0] = dot4(q1, s0, acc[1][0]);
-                acc[1][1] = dot4(q1, s1, acc[1][1]);
+                const float4 q0 = load4(sm.q + ti * LK + c), q1 = load4(sm.q + (ti + 16) * LK + c);
+                const float4 s0 = load4(sm.S + tj * LK + c), s1 = load4(sm.S + (tj + 16) * LK + c);
+                dot4(q0, s0, part[0][0]);
+                dot4(q0, s1, part[0][1]);
+                dot4(q1, s0, part[1][0]);
+                dot4(q1, s1, part[1][1]);
             }
+            float2 sum[2];  // token x: channels tj, tj + 16
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) acc[x][y] *= sm.e[ti + 16 * x];
-            for (int j = 0; j < L; ++j) {
-                const float v0 = sm.v[j * LV + tj], v1 = sm.v[j * LV + tj + 16];
+            for (int x = 0; x < 2; ++x) {
+                const float e = sm.e[ti + 16 * x];
+                sum[x] = make_float2(e * (part[x][0].x + part[x][0].y), e * (part[x][1].x + part[x][1].y));
+            }
+#pragma unroll 8
+            for (int j = 0; j < kC; ++j) {  // (rows from L on are zeros)
+                const float2 vv = make_float2(sm.v[j * LV + tj], sm.v[j * LV + tj + 16]);
                 const float p0 = sm.P[ti * LP + j], p1 = sm.P[(ti + 16) * LP + j];
-                acc[0][0] = fmaf(p0, v0, acc[0][0]);
-                acc[0][1] = fmaf(p0, v1, acc[0][1]);
-                acc[1][0] = fmaf(p1, v0, acc[1][0]);
-                acc[1][1] = fmaf(p1, v1, acc[1][1]);
+                sum[0] = __ffma2_rn(make_float2(p0, p0), vv, sum[0]);
+                sum[1] = __ffma2_rn(make_float2(p1, p1), vv, sum[1]);
             }
+            const float acc[2][2] = {{sum[0].x, sum[0].y}, {sum[1].x, sum[1].y}};
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -182,17 +210,16 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
         __syncthreads();
         // S = 2^G S + sum_j w_j v_j k_j^T
         {
-            float acc[TR][4] = {};
-            for (int j = 0; j < L; ++j) {
-                const float4 kk = *reinterpret_cast<const float4 *>(sm.k + j * LK + sc);
+            float2 acc[TR][2] = {};
+#pragma unroll 8
+            for (int j = 0; j < kC; ++j) {
+                const float4 kk = load4(sm.k + j * LK + sc);
                 const float w = sm.w[j];
 #pragma unroll
                 for (int i = 0; i < TR; ++i) {
                     const float x = w * sm.v[j * LV + sr + i];
-                    acc[i][0] = fmaf(x, kk.x, acc[i][0]);
-                    acc[i][1] = fmaf(x, kk.y, acc[i][1]);
-                    acc[i][2] = fmaf(x, kk.z, acc[i][2]);
-                    acc[i][3] = fmaf(x, kk.w, acc[i][3]);
+                    acc[i][0] = __ffma2_rn(make_float2(x, x), make_float2(kk.x, kk.y), acc[i][0]);
+                    acc[i][1] = __ffma2_rn(make_float2(x, x), make_float2(kk.z, kk.w), acc[i][1]);
                 }
             }
             const float2 d = sm.decay;
@@ -202,10 +229,10 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
             for (int i = 0; i < TR; ++i) {
                 float4 *p = reinterpret_cast<float4 *>(sm.S + (sr + i) * LK + sc);
                 float4 x = *p;
-                x.x = fmaf(d.x, x.x, fmaf(d.y, x.x, acc[i][0]));
-                x.y = fmaf(d.x, x.y, fmaf(d.y, x.y, acc[i][1]));
-                x.z = fmaf(d.x, x.z, fmaf(d.y, x.z, acc[i][2]));
-                x.w = fmaf(d.x, x.w, fmaf(d.y, x.w, acc[i][3]));
+                x.x = fmaf(d.x, x.x, fmaf(d.y, x.x, acc[i][0].x));
+                x.y = fmaf(d.x, x.y, fmaf(d.y, x.y, acc[i][0].y));
+                x.z = fmaf(d.x, x.z, fmaf(d.y, x.z, acc[i][1].x));
+                x.w = fmaf(d.x, x.w, fmaf(d.y, x.w, acc[i][1].y));
                 *p = x;
                 if (snap)
                     *reinterpret_cast<float4 *>(
@@ -244,14 +271,24 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a,
     const Tin *v = static_cast<const Tin *>(a.v) + (s.start * a.H + h) * dv + r0;
     const int64_t ldk = a.Hk * DK, ldv = a.H * dv;
     const int sc = tid % (DK / 4) * 4, sr = tid / (DK / 4) * TR;
-    float acc[TR][4] = {};
+    float2 acc[TR][2] = {};
     float after_chunk = 0.f;  // sum of the gates after the chunk
+    Rows<DK, LK, Tin> kn;     // the chunk before, on its way
+    Rows<kRows, LV, Tin> vn;
+    float gn = 0.f;
+    auto ahead = [&](int64_t t0) {
+        kn.read(k + t0 * ldk, ldk, kC);
+        vn.read(v + t0 * ldv, ldv, kC);
+        if (warp == 0) gn = gate2(a, fixed, s.start + t0 + lane, h);
+    };
+    ahead(s.len - kC);
     for (int64_t t0 = s.len - kC; t0 >= 0 && after_chunk > kDead; t0 -= kC) {  // (segments here are whole chunks)
         __syncthreads();
-        stage_rows<DK, LK>(ks, k + t0 * ldk, ldk, kC);
-        stage_rows<kRows, LV>(vs, v + t0 * ldv, ldv, kC);
+        kn.put(ks);
+        vn.put(vs);
+        const float g = gn;
+        if (t0 >= kC) ahead(t0 - kC);
         if (warp == 0) {
-            const float g = gate2(a, fixed, s.start + t0 + lane, h);
             float G, after;
             warp_scans(g, lane, G, after);
             ws[lane] = ex2(after + after_chunk);
@@ -259,16 +296,15 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a,
         }
         __syncthreads();
         after_chunk += s_total;
+#pragma unroll 8
         for (int j = 0; j < kC; ++j) {
-            const float4 kk = *reinterpret_cast<const float4 *>(ks + j * LK + sc);
+            const float4 kk = load4(ks + j * LK + sc);
             const float w = ws[j];
 #pragma unroll
             for (int i = 0; i < TR; ++i) {
                 const float x = w * vs[j * LV + sr + i];
-                acc[i][0] = fmaf(x, kk.x, acc[i][0]);
-                acc[i][1] = fmaf(x, kk.y, acc[i][1]);
-                acc[i][2] = fmaf(x, kk.z, acc[i][2]);
-                acc[i][3] = fmaf(x, kk.w, acc[i][3]);
+                acc[i][0] = __ffma2_rn(make_float2(x, x), make_float2(kk.x, kk.y), acc[i][0]);
+                acc[i][1] = __ffma2_rn(make_float2(x, x), make_float2(kk.z, kk.w), acc[i][1]);
             }
         }
     }
@@ -276,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a,
 #pragma unroll
     for (int i = 0; i < TR; ++i)
         *reinterpret_cast<float4 *>(U + (int64_t)(r0 + sr + i) * DK + sc) =
-            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
     // the segment's decay (once it is past kDead, how far past does not matter)
     if (r0 == 0 && tid == 0) {
         a.alive[s.ss * a.H + h] = 1;

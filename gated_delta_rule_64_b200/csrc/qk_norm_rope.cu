@@ -20,7 +20,7 @@ namespace gdn {
 namespace lin {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Quad {
     float2 a, b;
@@ -57,12 +57,13 @@ struct RopeArgs {
     void *q_out, *k_out;
     int64_t rows, q_stride, k_stride;
     int hq, hk, rot, tokens;  // tokens: per block, a power of two
+    int half_bits;            // 2^half_bits >= rot / 2
     bool interleaved;
     float eps, offset;
 };
 
 template <int D, typename Tin, bool INTER>
-__global__ void __launch_bounds__(kThreads, 4) gdn_qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const RopeArgs a) {
     constexpr int kGroup = D / 8;               // lanes of a head
     constexpr int kGroups = kThreads / kGroup;  // of a block; as many tokens at most
     __shared__ __align__(16) float s_cos[kGroups * D / 2], s_sin[kGroups * D / 2];
@@ -92,9 +93,15 @@ __global__ void __launch_bounds__(kThreads, 4) gdn_qk_norm_rope_kernel(const Rop
         y0 = load_quad(q + step * D + c0);
         y1 = load_quad(q + step * D + c1);
     }
-    for (int i = tid; i < tokens * half; i += kThreads) {
-        const double turn = (double)a.pos[row0 + i / half] * (double)a.inv_freq[i % half] * 0.15915494309189533577;
-        sincospif((float)(2.0 * (turn - rint(turn))), &s_sin[i], &s_cos[i]);
+    if (half > 0) {  // a thread takes one frequency, of every (128 / width)-th token
+        const int i = tid & ((1 << a.half_bits) - 1), stride = kThreads >> a.half_bits;
+        if (i < half) {
+            const double f = (double)a.inv_freq[i] * 0.15915494309189533577;
+            for (int u = tid >> a.half_bits; u < tokens; u += stride) {
+                const double turn = (double)a.pos[row0 + u] * f;
+                sincospif((float)(2.0 * (turn - rint(turn))), &s_sin[u * half + i], &s_cos[u * half + i]);
+            }
+        }
     }
     __syncthreads();
     Quad cs = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -190,8 +197,9 @@ gdn_status launch_d(const gdn_qk_rope_desc &d, RopeArgs &a, cudaStream_t s) {
 gdn_status launch_qk_norm_rope(const gdn_qk_rope_desc &d, const void *q, const void *k, const int32_t *pos,
                                const float *inv_freq, const float *qw, const float *kw, void *q_out, void *k_out,
                                cudaStream_t s) {
-    RopeArgs a{q, k, pos, inv_freq, qw, kw, q_out, k_out, d.rows, d.q_stride, d.k_stride, d.hq, d.hk, d.rot, 1,
+    RopeArgs a{q, k, pos, inv_freq, qw, kw, q_out, k_out, d.rows, d.q_stride, d.k_stride, d.hq, d.hk, d.rot, 1, 0,
                d.interleaved != 0, d.eps, d.weight_offset};
+    while ((1 << a.half_bits) < d.rot / 2) ++a.half_bits;
     return d.head_dim == 64 ? launch_d<64>(d, a, s) : d.head_dim == 128 ? launch_d<128>(d, a, s) : launch_d<256>(d, a, s);
 }
 
