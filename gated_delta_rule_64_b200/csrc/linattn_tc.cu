@@ -297,8 +297,8 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     constexpr int kIssuerS = 16, kIssuerO = 17, kStorer = 18, kLoader = 19;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 2);  // both issuing warps
+            mbar_init(&bars.full[i], 1 + 32);  // the loads, and the chunk's factors
+            mbar_init(&bars.empty[i], 2);      // both issuing warps
         }
         for (int i = 0; i < kRing; ++i) mbar_init(&bars.fac[i], 32);
         for (int i = 0; i < 2; ++i) {
@@ -451,8 +451,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             uint8_t *st = sm + stage * kStage;
             const Factors &fac = ring[c % kRing];
             const int L = (int)(s.len - (int64_t)c * C < C ? s.len - (int64_t)c * C : C);
-            ok = warp_wait(&bars.fac[c % kRing], (c / kRing) & 1);
-            ok = ok && warp_wait(&bars.full[stage], (c / kStages) & 1);
+            ok = warp_wait(&bars.full[stage], (c / kStages) & 1);  // (the factors too)
             if (!ok) break;
             if (L < C) {  // rows behind the sequence: whatever lies there stays out of the sums
                 for (int i = tid - 256; i < 64 * 8; i += 128)
@@ -706,6 +705,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                                                 : exp2_pair((double)a.g[h] * 1.4426950408889634074 * (double)left));
             }
             mbar_arrive(&bars.fac[c % kRing]);
+            mbar_arrive(&bars.full[stage]);
         }
     }
     __syncwarp();
