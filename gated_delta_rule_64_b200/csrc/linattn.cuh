@@ -112,6 +112,27 @@ __device__ __forceinline__ float2 exp2_pair(double x) {
     return make_float2(hi, (float)(e - (double)hi));
 }
 
+// The kernels of a call overlap at their ends: each lets the next one start (early), and the
+// next one waits for it before it touches what it wrote, in every block, so that the stream's
+// order holds for what follows the call.  The first kernel of a call is launched as usual.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool after_previous,
+                          A... args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = block;
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &attr;
+    c.numAttrs = after_previous ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 gdn_status launch_simt(const Plan &p, const Args &a, int dtype, cudaStream_t s);
 gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s);
 gdn_status launch_combine(const Plan &p, const Args &a, cudaStream_t s);

@@ -40,7 +40,8 @@ static int64_t choose_seg(int64_t N, int64_t units, int64_t T, int64_t rows, boo
     auto waves = [wide](int64_t blocks) { return (double)((blocks + wide - 1) / wide); };
     int64_t best = nch;
     double best_cost = waves(N * units) * ((double)nch + kStart);
-    for (int64_t G = 2; G <= 1024; ++G) {
+    // (more than 16 waves of blocks are never better)
+    for (int64_t G = 2; G <= nch && (G == 2 || N * units * G <= 16 * wide); ++G) {
         const int64_t seg = (nch + G - 1) / G;
         if (seg < kLeast) break;
         const int64_t Gr = (nch + seg - 1) / seg;  // no empty segments
@@ -71,7 +72,7 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
-        cudaGetLastError();
+        cudaGetLastError();  // (no device: sizes are planned for the GPU this library is built for)
         sms = 148;
     }
     const int64_t units = p.tc ? p.H : p.H * (p.dv / 32), wide = p.tc ? sms : 2 * sms;

@@ -108,7 +108,10 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
     const int64_t h = id / slices % a.H;
     const int r0 = (int)(id % slices) * kRows;
     Slot s;
-    if (!locate<false>(a, id / slices / a.H, s)) return;
+    if (!locate<false>(a, id / slices / a.H, s)) {
+        wait_for_previous();
+        return;
+    }
     const int64_t hq = h / (a.H / a.Hk);
     const Tin *q = static_cast<const Tin *>(a.q) + (s.start * a.Hk + hq) * DK;
     const Tin *k = static_cast<const Tin *>(a.k) + (s.start * a.Hk + hq) * DK;
@@ -119,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
     const int sc = tid % (DK / 4) * 4, sr = tid / (DK / 4) * TR;
     const float *from = s.nseg > 1 ? a.states + (s.ss * a.H + h) * dv * DK
                                    : (a.h0 ? a.h0 + (s.n * a.H + h) * dv * DK : nullptr);
+    wait_for_previous();
 #pragma unroll
     for (int i = 0; i < TR; ++i)
         *reinterpret_cast<float4 *>(sm.S + (sr + i) * LK + sc) =
@@ -259,6 +263,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a,
     __shared__ __align__(16) float vs[kC * LV];
     __shared__ float ws[kC];
     __shared__ float s_total;
+    let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slices = (int)(dv / kRows);
     const int64_t id = blockIdx.x;
@@ -331,6 +336,8 @@ __global__ void __launch_bounds__(kCombThreads) gdn_linattn_combine(const Args a
     __shared__ uint32_t s_alive[kCombSegs];  // a bit per part (of the first kCombParts)
     const int64_t h = blockIdx.y, e = ((int64_t)blockIdx.z * kCombThreads + threadIdx.x) * 4;
     const int tid = threadIdx.x, parts = (int)a.parts;
+    let_next_start();
+    wait_for_previous();
     for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
         int64_t start, len;
         seq_bounds(a.cu, n, a.T, a.rows, start, len);
@@ -402,7 +409,8 @@ gdn_status launch_dk(const Plan &p, const Args &a, cudaStream_t s) {
     {
         log_launch("gdn_linattn_simt", dim3((unsigned)grid), dim3(kThreads), smem);
         LaunchScope ls("gdn_linattn_simt", s);
-        gdn_linattn_simt<DK, Tin><<<(unsigned)grid, kThreads, smem, s>>>(a, p.dv, p.fixed_gate);
+        launch_kernel(gdn_linattn_simt<DK, Tin>, dim3((unsigned)grid), dim3(kThreads), smem, s, sgrid > 0, a, p.dv,
+                      p.fixed_gate);
     }
     return check_launch("gdn_linattn_simt");
 }
@@ -416,7 +424,7 @@ gdn_status launch_combine(const Plan &p, const Args &a, cudaStream_t s) {
                     (unsigned)((elems + 4 * kCombThreads - 1) / (4 * kCombThreads)));
     log_launch("gdn_linattn_combine", grid, dim3(kCombThreads), 0);
     LaunchScope ls("gdn_linattn_combine", s);
-    gdn_linattn_combine<<<grid, kCombThreads, 0, s>>>(a, elems);
+    launch_kernel(gdn_linattn_combine, grid, dim3(kCombThreads), 0, s, true, a, elems);
     return check_launch("gdn_linattn_combine");
 }
 

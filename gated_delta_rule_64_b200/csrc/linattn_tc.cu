@@ -291,8 +291,11 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t h = blockIdx.x % a.H;
     Slot s;
-    if (!locate<false>(a, blockIdx.x / a.H, s)) return;
-    if (!in_bounds(s.start >= 0 && s.start + s.len <= a.rows && s.n < a.N && h < a.H, a.status)) return;
+    if (!locate<false>(a, blockIdx.x / a.H, s) ||
+        !in_bounds(s.start >= 0 && s.start + s.len <= a.rows && s.n < a.N && h < a.H, a.status)) {
+        wait_for_previous();
+        return;
+    }
     const int nch = (int)((s.len + C - 1) / C);
     constexpr int kIssuerS = 16, kIssuerO = 17, kStorer = 18, kLoader = 19;
     if (tid == 0) {
@@ -340,6 +343,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const float *from = s.nseg > 1 ? a.states + (s.ss * a.parts * a.H + h) * (int64_t)(D * D)
                                        : (a.h0 ? a.h0 + (s.n * a.H + h) * (int64_t)(D * D) : nullptr);
         float S[64];
+        wait_for_previous();  // (the other roles need nothing that earlier kernels of the call wrote)
         if (from) {
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
@@ -804,6 +808,7 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
     constexpr int kIssuer = kTermWarps, kLoader = kTermWarps + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t h = blockIdx.x % a.H, unit = blockIdx.x / a.H;
+    let_next_start();
     // (the newest parts of all segments first: the blocks that find nothing to do come last)
     const int64_t part = a.parts - 1 - unit / a.sslots;
     Slot s;
@@ -1029,7 +1034,8 @@ gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s) {
     {
         log_launch("gdn_linattn_tc", dim3((unsigned)grid), dim3(kOutThreads), kOutSmem);
         LaunchScope ls("gdn_linattn_tc", s);
-        gdn_linattn_tc<<<(unsigned)grid, kOutThreads, kOutSmem, s>>>(mq, mk, mv, mo, a, p.fixed_gate);
+        launch_kernel(gdn_linattn_tc, dim3((unsigned)grid), dim3(kOutThreads), kOutSmem, s, sgrid > 0, mq, mk, mv, mo, a,
+                      p.fixed_gate);
     }
     return check_launch("gdn_linattn_tc");
 }
