@@ -11,9 +11,13 @@
 // U = sum_j 2^{(decay from j to the segment's end)} v_j k_j^T whatever state it starts
 // from.  So a long sequence is cut into segments of `seg` tokens: the state kernel
 // forms every segment's U (all segments but each sequence's last, from its end
-// backwards until nothing reaches the end any more), the combine kernel chains the start states
-// S_{g+1} = 2^{G_g} S_g + U_g, and the output kernel runs all segments side by side.
-// Sequences of one segment need the output kernel alone.
+// backwards until nothing reaches the end any more; in one or more parts, whose U add up),
+// and the output kernel runs all segments side by side, each from
+//     S_g = U_{g-1} + 2^{G_{g-1}} (U_{g-2} + 2^{G_{g-2}} ( .. )):
+// its blocks add that up themselves, newest first, until the decay has left nothing.  Where
+// many segments could take part (kMostChained) the combine kernel chains the start
+// states S_{g+1} = 2^{G_g} S_g + U_g first.  Sequences of one segment need the output kernel
+// alone.
 #pragma once
 
 #include "chunk_common.cuh"
@@ -30,6 +34,7 @@ constexpr float kDead = -150.f;
 struct Plan {
     int64_t N, rows, T, H, Hk, dk, dv;
     bool packed, tc, fixed_gate;
+    bool chained;    // the output kernel's blocks add up their start states
     int64_t seg;     // tokens per segment, a multiple of 64
     int64_t G;       // fixed-length sequences: segments per sequence (>= 1)
     int64_t slots;   // segments in all (packed: an upper bound)
@@ -37,6 +42,7 @@ struct Plan {
     int64_t parts, part_len;  // blocks of the state kernel per segment, and their tokens
     size_t off_status, off_tot, off_alive, off_state, total;
 };
+constexpr int64_t kMostChained = 128;  // U that a block of the output kernel adds up at most
 constexpr int64_t kMaxPart = 16384;  // tokens of a part (their weights lie in shared memory)
 constexpr int64_t kMostParts = 32;   // of a segment (the combine kernel keeps a bit for each)
 Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed);
@@ -47,6 +53,7 @@ struct Args {
     const int32_t *cu;
     int64_t T, N, rows, H, Hk, seg, G, slots, sslots, parts, part_len;
     float scale;
+    bool chained;
     int64_t snap_stride, n_snap;
     void *out;
     float *final_state, *snaps;
@@ -131,6 +138,25 @@ cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t sm
     c.attrs = &attr;
     c.numAttrs = after_previous ? 1 : 0;
     return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
+// Start state of segment `s` of head h, `elems` values per state: `take(f, src)` is called for
+// every state of `elems` floats at src that has a part in it, times f (two floats), by
+// every thread that calls this.
+template <typename Take>
+__device__ __forceinline__ void start_state(const Args &a, const Slot &s, int64_t h, int64_t elems, Take take) {
+    if (s.j > 0 && !a.chained) return take(make_float2(1.f, 0.f), a.states + (s.ss * a.parts * a.H + h) * elems);
+    double decay = 0.0;  // log2, from the end of segment j to the start of this one
+    for (int64_t j = s.j - 1; j >= 0; --j) {
+        const float2 f = exp2_pair(decay);
+        if (f.x == 0.f) return;
+        const int64_t ss = s.ss - s.j + j;
+        for (int64_t i = 0; i < a.parts; ++i)
+            if (a.alive[(ss * a.parts + i) * a.H + h]) take(f, a.states + ((ss * a.parts + i) * a.H + h) * elems);
+        decay += a.tot[ss * a.H + h];
+    }
+    const float2 f = s.j == 0 ? make_float2(1.f, 0.f) : exp2_pair(decay);
+    if (a.h0 && f.x != 0.f) take(f, a.h0 + (s.n * a.H + h) * elems);
 }
 
 gdn_status launch_simt(const Plan &p, const Args &a, int dtype, cudaStream_t s);

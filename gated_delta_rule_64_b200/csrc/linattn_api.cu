@@ -103,6 +103,7 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
     if (parts < least) parts = least;
     p.parts = p.tc && parts > 1 ? parts : 1;
     p.part_len = (chunks + p.parts - 1) / p.parts * kChunk;
+    p.chained = (packed ? (p.rows + p.seg - 1) / p.seg : p.G) * p.parts <= kMostChained;
     size_t off = 0;
     p.off_status = off;
     off += kStatusBytes;
@@ -219,6 +220,7 @@ gdn_status gdn_linattn_chunk_fwd(const gdn_desc *d, const void *q, const void *k
     a.sslots = p.sslots;
     a.parts = p.parts;
     a.part_len = p.part_len;
+    a.chained = p.chained;
     a.scale = d->scale;
     a.snap_stride = snapshot_stride;
     a.n_snap = n_snap;

@@ -120,14 +120,6 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
     const int64_t ldk = a.Hk * DK, ldv = a.H * dv;
     // this thread's part of the state: rows sr .. sr + TR - 1, columns sc .. sc + 3
     const int sc = tid % (DK / 4) * 4, sr = tid / (DK / 4) * TR;
-    const float *from = s.nseg > 1 ? a.states + (s.ss * a.H + h) * dv * DK
-                                   : (a.h0 ? a.h0 + (s.n * a.H + h) * dv * DK : nullptr);
-    wait_for_previous();
-#pragma unroll
-    for (int i = 0; i < TR; ++i)
-        *reinterpret_cast<float4 *>(sm.S + (sr + i) * LK + sc) =
-            from ? load4(from + (int64_t)(r0 + sr + i) * DK + sc) : make_float4(0.f, 0.f, 0.f, 0.f);
-
     Rows<DK, LK, Tin> qn, kn;  // the next chunk's, on their way while the current one is worked on
     Rows<kRows, LV, Tin> vn;
     float gn = 0.f;
@@ -138,6 +130,22 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
         gn = warp == 0 && t0 + lane < s.len ? gate2(a, fixed, s.start + t0 + lane, h) : 0.f;
     };
     if (s.len > 0) ahead(0);
+    wait_for_previous();
+    {
+        float4 x[TR] = {};
+        start_state(a, s, h, dv * DK, [&](float2 f, const float *src) {
+#pragma unroll
+            for (int i = 0; i < TR; ++i) {
+                const float4 y = load4(src + (int64_t)(r0 + sr + i) * DK + sc);
+                x[i].x = fmaf(f.x, y.x, fmaf(f.y, y.x, x[i].x));
+                x[i].y = fmaf(f.x, y.y, fmaf(f.y, y.y, x[i].y));
+                x[i].z = fmaf(f.x, y.z, fmaf(f.y, y.z, x[i].z));
+                x[i].w = fmaf(f.x, y.w, fmaf(f.y, y.w, x[i].w));
+            }
+        });
+#pragma unroll
+        for (int i = 0; i < TR; ++i) *reinterpret_cast<float4 *>(sm.S + (sr + i) * LK + sc) = x[i];
+    }
     for (int64_t t0 = 0; t0 < s.len; t0 += kC) {
         const int L = (int)(s.len - t0 < kC ? s.len - t0 : kC);
         __syncthreads();  // the previous chunk is done with the tiles
@@ -404,7 +412,7 @@ gdn_status launch_dk(const Plan &p, const Args &a, cudaStream_t s) {
             gdn_linattn_state_simt<DK, Tin><<<(unsigned)sgrid, kThreads, 0, s>>>(a, p.dv, p.fixed_gate);
         }
         if ((st = check_launch("gdn_linattn_state_simt")) != GDN_OK) return st;
-        if ((st = launch_combine(p, a, s)) != GDN_OK) return st;
+        if (!p.chained && (st = launch_combine(p, a, s)) != GDN_OK) return st;
     }
     {
         log_launch("gdn_linattn_simt", dim3((unsigned)grid), dim3(kThreads), smem);

@@ -340,20 +340,20 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int qd = warp & 3, hf = warp >> 2, v = qd * 32 + lane;
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
         const int64_t srow = (int64_t)v * D + 64 * hf;
-        const float *from = s.nseg > 1 ? a.states + (s.ss * a.parts * a.H + h) * (int64_t)(D * D)
-                                       : (a.h0 ? a.h0 + (s.n * a.H + h) * (int64_t)(D * D) : nullptr);
         float S[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) S[c] = 0.f;
         wait_for_previous();  // (the other roles need nothing that earlier kernels of the call wrote)
-        if (from) {
+        start_state(a, s, h, (int64_t)(D * D), [&](float2 f, const float *src) {
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(from + srow + c);
-                S[c] = t.x; S[c + 1] = t.y; S[c + 2] = t.z; S[c + 3] = t.w;
+                const float4 t = *reinterpret_cast<const float4 *>(src + srow + c);
+                S[c] = fmaf(f.x, t.x, fmaf(f.y, t.x, S[c]));
+                S[c + 1] = fmaf(f.x, t.y, fmaf(f.y, t.y, S[c + 1]));
+                S[c + 2] = fmaf(f.x, t.z, fmaf(f.y, t.z, S[c + 2]));
+                S[c + 3] = fmaf(f.x, t.w, fmaf(f.y, t.w, S[c + 3]));
             }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) S[c] = 0.f;
-        }
+        });
         auto publish = [&] {  // S0 as bf16 pairs: this thread's 32 columns of the A operand
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1029,7 +1029,7 @@ gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s) {
             gdn_linattn_state_tc<<<(unsigned)sgrid, kStateThreads, state_smem, s>>>(mk, mv, a, p.fixed_gate);
         }
         if ((st = check_launch("gdn_linattn_state_tc")) != GDN_OK) return st;
-        if ((st = launch_combine(p, a, s)) != GDN_OK) return st;
+        if (!p.chained && (st = launch_combine(p, a, s)) != GDN_OK) return st;
     }
     {
         log_launch("gdn_linattn_tc", dim3((unsigned)grid), dim3(kOutThreads), kOutSmem);

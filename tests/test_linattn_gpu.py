@@ -89,6 +89,14 @@ def test_chunk_long_split_with_snapshots(dtype, d, gate, decay):
     _check(x, snapshot_stride=192)
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+@pytest.mark.parametrize("gate,decay", [("token", 1.0), ("token", 0.002), ("const", 0.0)])
+def test_chunk_very_many_segments(dtype, d, gate, decay):
+    """One head over 40,000 tokens: so many segments that their start states are chained by a kernel of
+    their own; a weak decay carries every segment's state into all that follow."""
+    _check(_inputs(1, 40_000, 1, 1, d, d, dtype, gate, seed=16, decay=decay))
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("gate,decay", [("token", 1.0), ("token", 0.01)])
 @pytest.mark.parametrize("lengths", [[5], [70, 1, 0, 300, 64, 129], [0, 0, 33], [2500, 3, 1100, 0, 64, 1024, 2049]])
