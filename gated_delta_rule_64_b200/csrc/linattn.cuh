@@ -82,15 +82,21 @@ __device__ __forceinline__ int64_t clamped_cu(const Args &a, int64_t n) {
 __device__ __forceinline__ int64_t state_base(const Args &a, int64_t n) {
     return a.cu ? 2 * clamped_cu(a, n) / a.seg : n * a.G;
 }
+// (The whole block calls it, with the same slot.)
 template <bool STATE>
 __device__ __forceinline__ bool locate(const Args &a, int64_t slot, Slot &s) {
     int64_t base;
     if (a.cu) {
         auto base_of = [&](int64_t n) { return STATE ? state_base(a, n) : clamped_cu(a, n) / a.seg + n; };
         int64_t lo = 0, hi = a.N;  // the last sequence whose first slot is not past `slot`
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) / 2;
-            if (base_of(mid) <= slot) lo = mid; else hi = mid;
+        if (a.N <= blockDim.x) {   // a thread looks at one sequence: one trip to memory
+            lo = __syncthreads_count(threadIdx.x < a.N && base_of(threadIdx.x) <= slot) - 1;
+            if (lo < 0) return false;
+        } else {
+            while (hi - lo > 1) {
+                const int64_t mid = (lo + hi) / 2;
+                if (base_of(mid) <= slot) lo = mid; else hi = mid;
+            }
         }
         s.n = lo;
         base = base_of(lo);

@@ -104,6 +104,13 @@ def test_chunk_packed(dtype, d, gate, decay, lengths):
     _check(_inputs(1, 0, 4, 2, d, d, dtype, gate, h0=True, seed=len(lengths), lengths=lengths, decay=decay))
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+def test_chunk_packed_many_sequences(dtype, d):
+    """More sequences than a block has threads, empty ones among them, and one of several segments."""
+    lengths = [(7 * n) % 5 for n in range(700)] + [3000] + [0, 2] * 30
+    _check(_inputs(1, 0, 1, 1, d, d, dtype, h0=True, seed=17, lengths=lengths, decay=0.05))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_chunk_strong_decays_and_resets(dtype):
     """Gates that erase the state (-1e4, -300) beside gates of zero: nothing overflows, nothing leaks."""
