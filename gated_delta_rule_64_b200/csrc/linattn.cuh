@@ -82,6 +82,21 @@ __device__ __forceinline__ int64_t clamped_cu(const Args &a, int64_t n) {
 __device__ __forceinline__ int64_t state_base(const Args &a, int64_t n) {
     return a.cu ? 2 * clamped_cu(a, n) / a.seg : n * a.G;
 }
+// Tokens per segment of a sequence of `len` tokens, and how many segments it has: packed
+// sequences are cut into equal segments of `seg` tokens or fewer (blocks of one length leave
+// less of the GPU idle at the end than full ones and remainders: 216 chunk steps against 228 on
+// the benchmark's eight sequences and 32 heads).
+__device__ __forceinline__ int64_t segment_length(const Args &a, int64_t len, int64_t &nseg) {
+    if (len <= 0) {
+        nseg = 1;
+        return a.seg;
+    }
+    nseg = (len + a.seg - 1) / a.seg;
+    if (!a.cu || nseg == 1) return a.seg;
+    const int64_t e = ((len + nseg - 1) / nseg + kChunk - 1) / kChunk * kChunk;
+    nseg = (len + e - 1) / e;
+    return e;
+}
 // (The whole block calls it, with the same slot.)
 template <bool STATE>
 __device__ __forceinline__ bool locate(const Args &a, int64_t slot, Slot &s) {
@@ -108,11 +123,11 @@ __device__ __forceinline__ bool locate(const Args &a, int64_t slot, Slot &s) {
     if (s.n >= a.N || s.j < 0) return false;
     int64_t start, len;
     seq_bounds(a.cu, s.n, a.T, a.rows, start, len);
-    s.nseg = len > 0 ? (len + a.seg - 1) / a.seg : 1;
+    const int64_t seg = segment_length(a, len, s.nseg);
     if (s.j >= s.nseg) return false;
-    s.pos = s.j * a.seg;
+    s.pos = s.j * seg;
     s.start = start + s.pos;
-    s.len = len - s.pos < a.seg ? len - s.pos : a.seg;
+    s.len = len - s.pos < seg ? len - s.pos : seg;
     s.ss = state_base(a, s.n) + s.j;
     return s.nseg == 1 || s.ss < a.sslots;  // (wrong offsets stay inside the workspace)
 }

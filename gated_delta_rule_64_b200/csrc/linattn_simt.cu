@@ -349,7 +349,9 @@ __global__ void __launch_bounds__(kCombThreads) gdn_linattn_combine(const Args a
     for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
         int64_t start, len;
         seq_bounds(a.cu, n, a.T, a.rows, start, len);
-        const int64_t nseg = (len + a.seg - 1) / a.seg, ss = state_base(a, n);
+        int64_t nseg;
+        segment_length(a, len, nseg);
+        const int64_t ss = state_base(a, n);
         if (nseg < 2 || ss + nseg > a.sslots) continue;
         float *states = a.states + (ss * parts * a.H + h) * elems + e;
         float4 S = a.h0 ? *reinterpret_cast<const float4 *>(a.h0 + (n * a.H + h) * elems + e) : make_float4(0.f, 0.f, 0.f, 0.f);
