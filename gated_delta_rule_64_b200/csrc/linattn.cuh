@@ -20,6 +20,8 @@
 // alone.
 #pragma once
 
+#include <atomic>
+
 #include "chunk_common.cuh"
 #include "gdn_internal.cuh"
 #include "gdn_linattn.h"
@@ -30,6 +32,19 @@ namespace lin {
 constexpr float kLog2e = 1.4426950408889634f;
 // A decay below 2^-150 gives exactly zero in fp32 (the kernels flush from 2^-126 on).
 constexpr float kDead = -150.f;
+
+// A gate in log2 units.  At 2^kDead and below nothing is left of anything, so lower gates (the
+// type's lowest value, -infinity) are taken as that: sums over a chunk stay finite and keep
+// the gates beside them.
+constexpr float kErase = -152.f;
+__device__ __forceinline__ float gate2(float g) {
+    const float x = g * kLog2e;
+    return x < kErase ? kErase : x;
+}
+__device__ __forceinline__ double gate2_exact(float g) {
+    const double x = (double)g * 1.4426950408889634074;
+    return x < (double)kErase ? (double)kErase : x;
+}
 
 struct Plan {
     int64_t N, rows, T, H, Hk, dk, dv;
@@ -53,7 +68,7 @@ struct Args {
     const int32_t *cu;
     int64_t T, N, rows, H, Hk, seg, G, slots, sslots, parts, part_len;
     float scale;
-    bool chained;
+    bool chained;  // (not where the final state replaces the initial one that other blocks still read)
     int64_t snap_stride, n_snap;
     void *out;
     float *final_state, *snaps;
@@ -145,6 +160,19 @@ __device__ __forceinline__ float2 exp2_pair(double x) {
 // order holds for what follows the call.  The first kernel of a call is launched as usual.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Dynamic shared memory above 48 KB for `kernel` on the current device, once a device (`done`: a bit
+// for each).
+inline gdn_status allow_smem(const void *kernel, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (e == cudaSuccess && (dev > 63 || !(done.load() & bit))) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess && dev <= 63) done.fetch_or(bit);
+    }
+    return e == cudaSuccess ? GDN_OK : fail(GDN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(e));
+}
+
 template <typename... P, typename... A>
 cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool after_previous,
                           A... args) {
@@ -166,7 +194,7 @@ cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t sm
 // every thread that calls this.
 template <typename Take>
 __device__ __forceinline__ void start_state(const Args &a, const Slot &s, int64_t h, int64_t elems, Take take) {
-    if (s.j > 0 && !a.chained) return take(make_float2(1.f, 0.f), a.states + (s.ss * a.parts * a.H + h) * elems);
+    if (s.nseg > 1 && !a.chained) return take(make_float2(1.f, 0.f), a.states + (s.ss * a.parts * a.H + h) * elems);
     double decay = 0.0;  // log2, from the end of segment j to the start of this one
     for (int64_t j = s.j - 1; j >= 0; --j) {
         const float2 f = exp2_pair(decay);

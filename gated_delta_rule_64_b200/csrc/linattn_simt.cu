@@ -24,8 +24,8 @@ constexpr int kRows = 32;     // state rows per block
 constexpr int kThreads = 256;
 
 // Gate g of token row `row` and head h, in log2 units.
-__device__ __forceinline__ float gate2(const Args &a, bool fixed, int64_t row, int64_t h) {
-    return a.g[fixed ? h : row * a.H + h] * kLog2e;
+__device__ __forceinline__ float gate_of(const Args &a, bool fixed, int64_t row, int64_t h) {
+    return gate2(a.g[fixed ? h : row * a.H + h]);
 }
 
 // Inclusive prefix sum over the warp, and the sum of what follows the lane.
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
         qn.read(q + t0 * ldk, ldk, s.len - t0);
         kn.read(k + t0 * ldk, ldk, s.len - t0);
         vn.read(v + t0 * ldv, ldv, s.len - t0);
-        gn = warp == 0 && t0 + lane < s.len ? gate2(a, fixed, s.start + t0 + lane, h) : 0.f;
+        gn = warp == 0 && t0 + lane < s.len ? gate_of(a, fixed, s.start + t0 + lane, h) : 0.f;
     };
     if (s.len > 0) ahead(0);
     wait_for_previous();
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_simt(const Args a, int64
             sm.w[lane] = ex2(after);
             sm.e[lane] = a.scale * ex2((float)G);
             // the chunk's decay: a fixed gate's product in 64 bits, a token gate's sum
-            if (lane == 31) sm.decay = exp2_pair(fixed ? (double)a.g[h] * 1.4426950408889634074 * L : G);
+            if (lane == 31) sm.decay = exp2_pair(fixed ? gate2_exact(a.g[h]) * L : G);
         }
         __syncthreads();
         // scores: this thread's tokens i = ti, ti + 16 against j = tj, tj + 16
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a,
     auto ahead = [&](int64_t t0) {
         kn.read(k + t0 * ldk, ldk, kC);
         vn.read(v + t0 * ldv, ldv, kC);
-        if (warp == 0) gn = gate2(a, fixed, s.start + t0 + lane, h);
+        if (warp == 0) gn = gate_of(a, fixed, s.start + t0 + lane, h);
     };
     ahead(s.len - kC);
     for (int64_t t0 = s.len - kC; t0 >= 0 && after_chunk > kDead; t0 -= kC) {  // (segments here are whole chunks)
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linattn_state_simt(const Args a,
     // the segment's decay (once it is past kDead, how far past does not matter)
     if (r0 == 0 && tid == 0) {
         a.alive[s.ss * a.H + h] = 1;
-        a.tot[s.ss * a.H + h] = fixed ? (double)a.g[h] * 1.4426950408889634074 * (double)s.len : (double)after_chunk;
+        a.tot[s.ss * a.H + h] = fixed ? gate2_exact(a.g[h]) * (double)s.len : (double)after_chunk;
     }
 }
 
@@ -403,10 +403,9 @@ gdn_status launch_dk(const Plan &p, const Args &a, cudaStream_t s) {
     const int64_t slices = p.dv / kRows, grid = p.slots * p.H * slices, sgrid = p.sslots * p.H * slices;
     if (grid > 0x7fffffffLL || sgrid > 0x7fffffffLL) return fail(GDN_ERR_UNSUPPORTED, "grid too large");
     constexpr size_t smem = sizeof(Smem<DK>);
-    static const cudaError_t attr = cudaFuncSetAttribute(gdn_linattn_simt<DK, Tin>,
-                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (attr != cudaSuccess) return fail(GDN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(attr));
-    gdn_status st = GDN_OK;
+    static std::atomic<uint64_t> smem_done{0};
+    gdn_status st = allow_smem((const void *)gdn_linattn_simt<DK, Tin>, smem, smem_done);
+    if (st != GDN_OK) return st;
     if (sgrid > 0) {
         {
             log_launch("gdn_linattn_state_simt", dim3((unsigned)sgrid), dim3(kThreads), 0);
@@ -414,7 +413,7 @@ gdn_status launch_dk(const Plan &p, const Args &a, cudaStream_t s) {
             gdn_linattn_state_simt<DK, Tin><<<(unsigned)sgrid, kThreads, 0, s>>>(a, p.dv, p.fixed_gate);
         }
         if ((st = check_launch("gdn_linattn_state_simt")) != GDN_OK) return st;
-        if (!p.chained && (st = launch_combine(p, a, s)) != GDN_OK) return st;
+        if (!a.chained && (st = launch_combine(p, a, s)) != GDN_OK) return st;
     }
     {
         log_launch("gdn_linattn_simt", dim3((unsigned)grid), dim3(kThreads), smem);

@@ -290,13 +290,20 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t h = blockIdx.x % a.H;
-    Slot s;
-    if (!locate<false>(a, blockIdx.x / a.H, s) ||
-        !in_bounds(s.start >= 0 && s.start + s.len <= a.rows && s.n < a.N && h < a.H, a.status)) {
-        wait_for_previous();
-        return;
+    // (kept in shared memory: a role reads of it what it needs when it needs it)
+    __shared__ Slot s;
+    {
+        Slot found;
+        if (!locate<false>(a, blockIdx.x / a.H, found) ||
+            !in_bounds(found.start >= 0 && found.start + found.len <= a.rows && found.n < a.N && h < a.H, a.status)) {
+            wait_for_previous();
+            return;
+        }
+        if (tid == 0) s = found;
+        __syncthreads();
     }
-    const int nch = (int)((s.len + C - 1) / C);
+    const int len = (int)s.len, nch = (len + C - 1) / C;
+    const int cut = len % C ? nch - 1 : -1;  // the chunk with rows behind the segment, if any
     constexpr int kIssuerS = 16, kIssuerO = 17, kStorer = 18, kLoader = 19;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -454,12 +461,11 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const int stage = c % kStages;
             uint8_t *st = sm + stage * kStage;
             const Factors &fac = ring[c % kRing];
-            const int L = (int)(s.len - (int64_t)c * C < C ? s.len - (int64_t)c * C : C);
             ok = warp_wait(&bars.full[stage], (c / kStages) & 1);  // (the factors too)
             if (!ok) break;
-            if (L < C) {  // rows behind the sequence: whatever lies there stays out of the sums
+            if (c == cut) {  // rows behind the sequence: whatever lies there stays out of the sums
                 for (int i = tid - 256; i < 64 * 8; i += 128)
-                    if ((i >> 3) >= L) {
+                    if ((i >> 3) >= len % C) {
                         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4 *>(st + kStK + i * 16) = z;
                         *reinterpret_cast<uint4 *>(st + kStK + kHalfQK + i * 16) = z;
@@ -602,6 +608,8 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             if (c < 0) continue;
             ok = warp_wait(&bars.state, par);  // S0 in place, the previous chunk's O read
             ok = ok && warp_wait(&bars.p[par], (c >> 1) & 1);
+            // (a last chunk's rows behind the sequence have to be cleared, as they are before its terms)
+            if (c == cut) ok = ok && warp_wait(&bars.terms[par], (c >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t st = base + (c % kStages) * kStage;
@@ -621,8 +629,8 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             ok = warp_wait(&bars.out_full[c & 1], (c >> 1) & 1);
             if (!ok) break;
             const uint8_t *o = sm + kOffO + (c & 1) * 16384;
-            const int64_t row = s.start + (int64_t)c * C, left = s.len - (int64_t)c * C;
-            if (left >= C) {
+            const int64_t row = s.start + (int64_t)c * C;
+            if (c != cut) {
                 if (lane == 0) {
                     tma_store_3d(&mo, o, 0, hv, (int32_t)row);
                     tma_store_3d(&mo, o + 8192, 64, hv, (int32_t)row);
@@ -632,7 +640,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
             } else {  // rows behind the sequence stay as they are
                 __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.out) + (row * a.H + h) * D;
-                for (int i = lane; i < (int)left * 16; i += 32) {
+                for (int i = lane; i < len % C * 16; i += 32) {
                     const int t = i >> 4, p = i & 15;
                     *reinterpret_cast<uint4 *>(to + t * a.H * D + 8 * p) =
                         *reinterpret_cast<const uint4 *>(o + (p >> 3) * 8192 + sw128_offset(t, p & 7));
@@ -648,24 +656,25 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         // Loads, and the gates' factors, two tokens per lane
         // ------------------------------------------------------------------
         const int32_t hq = (int32_t)(h / (a.H / a.Hk)), hv = (int32_t)h;
-        if (lane == 0) {
+        if (lane == 0 && nch > 0) {
             prefetch_tmap(&mq);
             prefetch_tmap(&mk);
             prefetch_tmap(&mv);
         }
-        const float gh = fixed ? a.g[h] * kLog2e : 0.f;
+        const float gh = fixed ? gate2(a.g[h]) : 0.f;
         // A head's gates lie H floats apart, a memory sector each: they are asked for early.
+        const float *gates = a.g + (fixed ? 0 : s.start * a.H + h);
         auto ask_gates = [&](int c) {
             if (c < nch && !fixed) {
-                const int64_t t = (int64_t)c * C + 2 * lane;
-                const float *p = a.g + (s.start + t) * a.H + h;
-                async_copy4(&gate_ring[c % kRing][2 * lane], t < s.len ? p : a.g, t < s.len);
-                async_copy4(&gate_ring[c % kRing][2 * lane + 1], t + 1 < s.len ? p + a.H : a.g, t + 1 < s.len);
+                const int t = c * C + 2 * lane;
+                const float *p = gates + (int64_t)t * a.H;
+                async_copy4(&gate_ring[c % kRing][2 * lane], t < len ? p : a.g, t < len);
+                async_copy4(&gate_ring[c % kRing][2 * lane + 1], t + 1 < len ? p + a.H : a.g, t + 1 < len);
             }
             async_commit();  // (a group per chunk, empty or not)
         };
         for (int c = 0; c < kGateAhead; ++c) ask_gates(c);
-        const float2 fixed_decay = fixed ? exp2_pair((double)a.g[h] * 1.4426950408889634074 * C) : make_float2(0.f, 0.f);
+        const float2 fixed_decay = fixed ? exp2_pair(gate2_exact(a.g[h]) * C) : make_float2(0.f, 0.f);
         for (int c = 0; c < nch; ++c) {
             const int stage = c % kStages;
             if (c >= kStages) ok = warp_wait(&bars.empty[stage], ((c / kStages) & 1) ^ 1);
@@ -688,10 +697,10 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             // slot's last readers (chunk c - 8) are done.
             ask_gates(c + kGateAhead);
             async_wait<kGateAhead>();  // (a lane reads what it copied itself)
-            const int64_t left = s.len - (int64_t)c * C;
+            const int left = len - c * C;
             float2 g = *reinterpret_cast<const float2 *>(&gate_ring[c % kRing][2 * lane]);
             g = fixed ? make_float2(2 * lane < left ? gh : 0.f, 2 * lane + 1 < left ? gh : 0.f)
-                      : make_float2(g.x * kLog2e, g.y * kLog2e);
+                      : make_float2(gate2(g.x), gate2(g.y));
             Factors &fac = ring[c % kRing];
             float2 G, after;
             float total;
@@ -706,7 +715,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 fac.far = far;
                 fac.decay = !fixed ? make_float2(ex2(total), 0.f)
                                    : (left >= C ? fixed_decay
-                                                : exp2_pair((double)a.g[h] * 1.4426950408889634074 * (double)left));
+                                                : exp2_pair(gate2_exact(a.g[h]) * (double)left));
             }
             mbar_arrive(&bars.fac[c % kRing]);
             mbar_arrive(&bars.full[stage]);
@@ -766,8 +775,8 @@ __device__ __forceinline__ float part_weights(const Args &a, const Slot &s, int6
         const int64_t t = t1 - kSpan + 2 * tid;  // this thread's tokens t, t + 1 (the last thread's are the newest)
         float2 g = make_float2(0.f, 0.f);
         if (tid < kTermThreads) {
-            if (t >= begin) g.x = a.g[(s.start + t) * a.H + h] * kLog2e;
-            if (t + 1 >= begin) g.y = a.g[(s.start + t + 1) * a.H + h] * kLog2e;
+            if (t >= begin) g.x = gate2(a.g[(s.start + t) * a.H + h]);
+            if (t + 1 >= begin) g.y = gate2(a.g[(s.start + t + 1) * a.H + h]);
         }
         float sum = g.x + g.y;  // of this lane and the lanes above it
 #pragma unroll
@@ -818,7 +827,7 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
     const int64_t begin = part * a.part_len;  // of the part, in the segment
     const int64_t end = begin + a.part_len < s.len ? begin + a.part_len : s.len;
     // the decay from the part's end to the segment's
-    const double g64 = fixed ? (double)a.g[h] * 1.4426950408889634074 : 0.0;
+    const double g64 = fixed ? gate2_exact(a.g[h]) : 0.0;
     int64_t first = 0;
     const float gap = fixed ? (float)(g64 * (double)(s.len - end))
                             : part_weights(a, s, h, end, s.len, 0.f, nullptr, s_sum, first);
@@ -1015,13 +1024,10 @@ gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s) {
         if ((st = make_map(&mo, a.out, p.rows, p.H)) != GDN_OK) return st;
     }
     const size_t state_smem = kSsOffW + (size_t)p.part_len * sizeof(float) + 1024;
-    static const cudaError_t attr = [] {
-        const cudaError_t e = cudaFuncSetAttribute(gdn_linattn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem);
-        return e != cudaSuccess ? e
-                                : cudaFuncSetAttribute(gdn_linattn_state_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (int)(kSsOffW + kMaxPart * sizeof(float) + 1024));
-    }();
-    if (attr != cudaSuccess) return fail(GDN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(attr));
+    static std::atomic<uint64_t> out_done{0}, state_done{0};
+    if ((st = allow_smem((const void *)gdn_linattn_tc, kOutSmem, out_done)) != GDN_OK) return st;
+    if ((st = allow_smem((const void *)gdn_linattn_state_tc, kSsOffW + kMaxPart * sizeof(float) + 1024, state_done)) != GDN_OK)
+        return st;
     if (sgrid > 0) {
         {
             log_launch("gdn_linattn_state_tc", dim3((unsigned)sgrid), dim3(kStateThreads), state_smem);
@@ -1029,7 +1035,7 @@ gdn_status launch_tc(const Plan &p, const Args &a, cudaStream_t s) {
             gdn_linattn_state_tc<<<(unsigned)sgrid, kStateThreads, state_smem, s>>>(mk, mv, a, p.fixed_gate);
         }
         if ((st = check_launch("gdn_linattn_state_tc")) != GDN_OK) return st;
-        if (!p.chained && (st = launch_combine(p, a, s)) != GDN_OK) return st;
+        if (!a.chained && (st = launch_combine(p, a, s)) != GDN_OK) return st;
     }
     {
         log_launch("gdn_linattn_tc", dim3((unsigned)grid), dim3(kOutThreads), kOutSmem);

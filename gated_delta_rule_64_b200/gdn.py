@@ -356,7 +356,8 @@ def gdn_state_select(step_states, accept, state, *, stream=None):
 
 def _where(stream, t, *others):
     """The (device index, raw stream) of a call: the device its tensors are on and `stream`, or the current
-    stream of that device."""
+    stream of that device.  Tensors that a given stream uses are recorded on it: their memory is not handed
+    out again before the call has run."""
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors (the library has no CPU path)")
     dev = t.get_device()
@@ -364,9 +365,13 @@ def _where(stream, t, *others):
         if o is not None and o.get_device() != dev:
             raise ValueError(f"tensors are on different devices: {t.device} and {o.device}")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device_index != dev:
+        return dev, torch.cuda.current_stream(dev).cuda_stream
+    if stream.device_index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+    if stream != torch.cuda.current_stream(dev):
+        for o in (t,) + others:
+            if o is not None:
+                o.record_stream(stream)
     return dev, stream.cuda_stream
 
 

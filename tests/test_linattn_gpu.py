@@ -123,6 +123,22 @@ def test_chunk_strong_decays_and_resets(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("erase", [torch.finfo(torch.float32).min, float("-inf"), -106.0])
+@pytest.mark.parametrize("T", [200, 3000])
+def test_chunk_gates_of_the_lowest_value(dtype, erase, T):
+    """Gates that erase the state do not take the decays beside them along (sums of such gates are not
+    finite); a fixed gate of that value leaves each token with itself."""
+    x = _inputs(1, T, 2, 1, 128, 128, dtype, seed=18, decay=0.1)
+    for t in (0, 5, 70, 71, 130, 191, 199):
+        x["g"][:, t] = erase
+    if T > 200:
+        x["g"][:, 1000:1003] = erase
+    _check(x)
+    x["g"] = torch.tensor([erase, -0.01])
+    _check(x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_chunk_rows_outside_sequences_and_their_neighbours(dtype):
     """Rows behind the last sequence stay as they were, and what lies there (NaN, infinities) reaches
     no result; neither does a NaN in another sequence."""
@@ -161,8 +177,11 @@ def test_chunk_final_state_in_place_and_continued(dtype, d):
     assert rel_l2(state, f) <= TOL_F32
 
 
-def test_chunk_long_in_place_split():
-    x = _inputs(1, 6000, 1, 1, 128, 128, "bf16", seed=15, decay=0.02)
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+@pytest.mark.parametrize("decay", [0.02, 0.0])
+def test_chunk_long_in_place_split(dtype, d, decay):
+    """The final state replaces the initial one, which every segment's start depends on."""
+    x = _inputs(1, 6000, 3, 1, d, d, dtype, seed=15, decay=decay)
     _, f, _ = L.linear_attention(x["q"], x["k"], x["v"], x["g"], x["h0"])
     state = x["h0"].cuda()
     gdn.gdn_linattn_chunk_fwd(*(x[n].cuda() for n in "qkvg"), state, final_state=state)
@@ -232,6 +251,25 @@ def test_chunk_two_streams_at_once_and_repeatable():
     for got in both:
         for (o, f, _), (o1, f1, _) in zip(got, alone):
             assert torch.equal(o, o1) and torch.equal(f, f1)
+
+
+def test_calls_on_a_given_stream_keep_their_tensors():
+    """Inputs freed right after a call on another stream are not overwritten before it has run: memory that
+    the current stream asks for next is not theirs."""
+    side = torch.cuda.Stream()
+    x = _inputs(1, 20_000, 4, 4, 128, 128, "bf16", seed=19)
+    o, f, _ = gdn.gdn_linattn_chunk_fwd(*(x[n].cuda() for n in "qkvg"), x["h0"].cuda())
+    torch.cuda.synchronize()
+    for _ in range(3):
+        args = [x[n].cuda() for n in "qkvg"] + [x["h0"].cuda()]
+        torch.cuda.synchronize()
+        got = gdn.gdn_linattn_chunk_fwd(*args, stream=side)
+        sizes = [a.shape for a in args]
+        del args
+        junk = [torch.full(s, 7.0, dtype=torch.bfloat16, device="cuda") for s in sizes]
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], o) and torch.equal(got[1], f)
+        del junk, got
 
 
 # ---------------------------------------------------------------------------
