@@ -412,7 +412,7 @@ def _addr(t):
 
 
 def gdn_linattn_workspace_size(B, T, H, dk, dv, num_seqs, *, dtype=torch.bfloat16, hk=0) -> int:
-    lib = load_library()
+    lib = _lib or load_library()
     d = make_desc(B, T, H, dk, dv, GDN_F32 if dtype == torch.float32 else GDN_BF16, False, 1.0, hk)
     n = ctypes.c_size_t(0)
     _check(lib, lib.gdn_linattn_workspace_size(ctypes.byref(d), int(num_seqs), ctypes.byref(n)))
@@ -425,7 +425,7 @@ def gdn_linattn_chunk_fwd(q, k, v, log_gate, initial_state=None, cu_seqlens=None
     o_t = S_t (scale q_t).  Shapes as gdn_chunk_fwd; log_gate (B,T,H), or (H,) for one fixed decay per head.
     final_state: True to allocate, a tensor to fill (may be initial_state), or None.
     Returns (out, final_state, snapshots).  gdn_chunk_status(workspace) reads the call's device status."""
-    lib = load_library()
+    lib = _lib or load_library()
     B, T, Hq, dk = q.shape
     H, dv = v.shape[-2], v.shape[-1]
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else B
@@ -476,7 +476,7 @@ def gdn_linattn_chunk_fwd(q, k, v, log_gate, initial_state=None, cu_seqlens=None
 def gdn_linattn_decode_step(q, k, v, log_gate, state, *, scale=1.0, out=None, stream=None):
     """One token of every live sequence of gdn_linattn_chunk_fwd's recurrence; `state` (B,H,dv,dk) fp32 is
     updated in place.  q, k (B,1,hk,dk) or (B,hk,dk); v (B,1,H,dv) or (B,H,dv); log_gate (B,[1,]H) or (H,)."""
-    lib = load_library()
+    lib = _lib or load_library()
     B, H, dv, dk = state.shape
     hk = q.shape[-2]
     code = _dtype_code(q)
@@ -487,14 +487,13 @@ def gdn_linattn_decode_step(q, k, v, log_gate, state, *, scale=1.0, out=None, st
     fixed = log_gate.dim() == 1
     _need("log_gate", log_gate, (H,) if fixed else ((B,) if log_gate.dim() == 2 else (B, 1)) + (H,), torch.float32)
     _need("state", state, (B, H, dv, dk), torch.float32)
-    if out is None:
-        with _On(q.get_device(), stream):
-            out = torch.empty((B, 1, H, dv), dtype=q.dtype, device=q.device)
-    elif out.numel() != B * H * dv or out.dtype != q.dtype or not out.is_contiguous():
+    if out is not None and (out.numel() != B * H * dv or out.dtype != q.dtype or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous (B, 1, H, dv) tensor of {q.dtype}")
     dev, raw = _where(stream, q, k, v, log_gate, state, out)
-    d = GdnDesc(B, 1, H, dk, dv, code, GDN_GATE_CONST if fixed else GDN_GATE_HEAD, float(scale), hk if hk != H else 0)
-    with _On(dev, None):
+    d = GdnDesc(B, 1, H, dk, dv, code, GDN_GATE_CONST if fixed else GDN_GATE_HEAD, scale, hk if hk != H else 0)
+    with _On(dev, stream):
+        if out is None:
+            out = torch.empty((B, 1, H, dv), dtype=q.dtype, device=q.device)
         st = lib.gdn_linattn_decode_step(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
                                          state.data_ptr(), out.data_ptr(), raw)
     if st != GDN_OK:
@@ -525,7 +524,7 @@ def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, *,
     heads side by side); positions (B,T) int32; inv_freq (rot/2,) fp32, or None: no rotation; the weights (d,)
     fp32 or None.  Pairs are (i, i + rot/2), or (2i, 2i+1) when `interleaved`.  Returns (q_out, k_out), dense;
     either may be its (dense) input."""
-    lib = load_library()
+    lib = _lib or load_library()
     B, T, hq, dim = q.shape
     hk = k.shape[2]
     code = _dtype_code(q)
@@ -566,7 +565,7 @@ def gdn_beam_select(logits, scores, K, *, out_scores=None, out_parent=None, out_
     scores[b, w] + log_softmax(logits[b, w])[t], best first, equals in index order.
     logits (B,W,V) fp32 or bf16 (rows of V values evenly spaced: a padded vocabulary may be sliced off);
     scores (B,W) fp32 or None (zeros).  Returns (scores (B,K) fp32, parent beam (B,K) int32, token (B,K) int32)."""
-    lib = load_library()
+    lib = _lib or load_library()
     B, W, V = logits.shape
     code = _dtype_code(logits)
     st = logits.stride()
@@ -609,7 +608,7 @@ def gdn_state_reorder(state, parent, *, stream=None):
     (b, parent[b, w]) as it was before the call; a parent outside 0 .. W-1 leaves its row.  `state`: a
     contiguous tensor of any type whose leading dimension is B * W (recurrent states, convolution histories;
     a row is a multiple of 16 bytes); parent (B, W) int32.  Returns state."""
-    lib = load_library()
+    lib = _lib or load_library()
     B, W = parent.shape
     _need("parent", parent, (B, W), torch.int32)
     if state.dim() < 1 or state.shape[0] != B * W or not state.is_contiguous():
