@@ -58,6 +58,7 @@ struct RopeArgs {
     int64_t rows, q_stride, k_stride;
     int hq, hk, rot, tokens;  // tokens: per block, a power of two
     int half_bits;            // 2^half_bits >= rot / 2
+    int step_bits;            // 2^step_bits groups of lanes share a token
     bool interleaved;
     float eps, offset;
 };
@@ -76,14 +77,14 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
     const int c0 = INTER ? 8 * sub : (partners ? 4 * sub : a.rot + 8 * (sub - half / 4));
     const int c1 = partners ? c0 + half : c0 + 4;
     // this group's token and heads: h0, h0 + step, ...
-    const int step = kGroups / a.tokens, t = group / step, h0 = group % step;
+    const int sb = a.step_bits, step = 1 << sb, t = group >> sb, h0 = group & (step - 1);
     const bool live = t < tokens;
     const int64_t row = row0 + (live ? t : 0);
 
     typedef typename Raw<Tin>::type raw;
     const int64_t qo = (int64_t)h0 * D;
     const Tin *q = static_cast<const Tin *>(a.q) + row * a.q_stride + qo, *k = static_cast<const Tin *>(a.k) + row * a.k_stride + qo;
-    const int nq = live && h0 < a.hq ? (a.hq - h0 + step - 1) / step : 0, nk = live && h0 < a.hk ? (a.hk - h0 + step - 1) / step : 0;
+    const int nq = live ? (a.hq - h0 + step - 1) >> sb : 0, nk = live ? (a.hk - h0 + step - 1) >> sb : 0;  // (0 past the last head)
     raw x0 = {}, x1 = {}, y0 = {}, y1 = {};
     if (nq > 0) {  // in flight while the angles are formed
         x0 = load_quad(q + c0);
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
             dst += step * D;
         }
     };
-    run(q, static_cast<Tin *>(a.q_out) + row * a.hq * D + qo, nq, (a.hq + step - 1) / step, a.qw);
+    run(q, static_cast<Tin *>(a.q_out) + row * a.hq * D + qo, nq, (a.hq + step - 1) >> sb, a.qw);
     if (a.hk > 0) {
         if (nk > 0) {
             x0 = load_quad(k + c0);
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
             y0 = load_quad(k + step * D + c0);
             y1 = load_quad(k + step * D + c1);
         }
-        run(k, static_cast<Tin *>(a.k_out) + row * a.hk * D + qo, nk, (a.hk + step - 1) / step, a.kw);
+        run(k, static_cast<Tin *>(a.k_out) + row * a.hk * D + qo, nk, (a.hk + step - 1) >> sb, a.kw);
     }
 }
 
@@ -182,6 +183,8 @@ gdn_status launch_d(const gdn_qk_rope_desc &d, RopeArgs &a, cudaStream_t s) {
     int tokens = 1;
     while (2 * tokens <= kGroups && tokens * heads < 8 * kGroups && d.rows / (2 * tokens) >= 296) tokens *= 2;
     a.tokens = tokens;
+    for (a.step_bits = 0; (tokens << a.step_bits) < kGroups; ++a.step_bits) {
+    }
     const unsigned grid = (unsigned)((d.rows + tokens - 1) / tokens);
     LaunchScope ls("gdn_qk_norm_rope_kernel", s);
     auto kern = d.dtype == GDN_BF16 ? (a.interleaved ? gdn_qk_norm_rope_kernel<D, __nv_bfloat16, true>
@@ -197,7 +200,7 @@ gdn_status launch_d(const gdn_qk_rope_desc &d, RopeArgs &a, cudaStream_t s) {
 gdn_status launch_qk_norm_rope(const gdn_qk_rope_desc &d, const void *q, const void *k, const int32_t *pos,
                                const float *inv_freq, const float *qw, const float *kw, void *q_out, void *k_out,
                                cudaStream_t s) {
-    RopeArgs a{q, k, pos, inv_freq, qw, kw, q_out, k_out, d.rows, d.q_stride, d.k_stride, d.hq, d.hk, d.rot, 1, 0,
+    RopeArgs a{q, k, pos, inv_freq, qw, kw, q_out, k_out, d.rows, d.q_stride, d.k_stride, d.hq, d.hk, d.rot, 1, 0, 0,
                d.interleaved != 0, d.eps, d.weight_offset};
     while ((1 << a.half_bits) < d.rot / 2) ++a.half_bits;
     return d.head_dim == 64 ? launch_d<64>(d, a, s) : d.head_dim == 128 ? launch_d<128>(d, a, s) : launch_d<256>(d, a, s);
