@@ -7,10 +7,14 @@
 //     O   = S0 Q^T + V^T P^T          128 x 64 (one accumulator)
 //     dS  = (V w)^T K                 128 x 128: the state's increment
 //
-// with P_ij = 2^{-G_j} QK_ij for j <= i and w_j = 2^{G - G_j}; then o_i = scale 2^{G_i} O_i
-// and S = 2^G S0 + dS.  Where the chunk's decay G is below 2^-100 the factors 2^{-G_j} would
-// leave the range: there P_ij = scale 2^{G_i - G_j} QK_ij, and the Q that S0 multiplies is
-// scaled by scale 2^{G_i} in place (one more rounding to bf16, of that product only).
+// with w_j = 2^{G - G_j}, P_ij = 2^{-m - G_j} QK_ij for j <= i and 2^{-m} S0 in the place of S0;
+// then o_i = scale 2^{m + G_i} O_i and S = 2^G S0 + dS.  m, half of the chunk's decay rounded to
+// a whole number, keeps the factors within 2^60 of 1 for decays down to 2^-120 (and so the
+// sums of q k v in range up to 2^67), and as a power of two it rounds nothing.  Where the decay
+// is below that, m = 0 and P_ij = scale 2^{G_i - G_j} QK_ij, and the Q that S0 multiplies is
+// scaled by scale 2^{G_i} in place (one more rounding to bf16, of that product only): slower, so
+// only for those (taken from 2^-60 on, by one head of sixteen with a fixed decay, it held up a
+// sequence of 262,144 tokens: 940 us in this kernel against 820).
 //
 // Rounding.  P and the copy of S0 that Q multiplies are rounded to bf16, once each,
 // like the output they go into.  The state itself keeps fp32: V w is split into three
@@ -31,7 +35,7 @@
 //                half of the time, at about 200 cycles a wait)
 //   warp 18      stores the outputs
 //   warp 19      TMA loads (three stages of 48 KB) and the factors that come from the gates
-// One block per SM: 205 KB of shared memory, all 512 TMEM columns.
+// One block per SM: 208 KB of shared memory, all 512 TMEM columns.
 //
 // The loops of the roles are kept short on purpose: every scheduler runs a warp of each, and
 // with them unrolled (about 40 KB of code) the instruction caches, not the tensor pipe, set
@@ -259,12 +263,13 @@ constexpr int kGateAhead = 6;
 constexpr int kRegState = 136, kRegP = 56, kRegRest = 56;
 static_assert(2 * kRegState + 96 + kRegP + kRegRest <= 5 * 96, "no more than the block was launched with");
 
-constexpr float kFarDecay = -100.f;  // log2 of a chunk's decay
+constexpr float kFarDecay = -120.f;  // log2 of a chunk's decay
 
 struct __align__(16) Factors {
-    // per token: prefix sum G; 2^{-G}; decay to the chunk's end; what O is multiplied by
+    // per token: prefix sum G; 2^{-m - G}; decay to the chunk's end; what O is multiplied by
     float G[C], f[C], w[C], e[C];
     float2 decay;  // of the chunk
+    __nv_bfloat162 shift;  // 2^{-m}, twice
     int far;       // the chunk's decay is below kFarDecay
 };
 // A barrier that one side may complete again before the other side has looked (terms and P are
@@ -337,6 +342,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const uint32_t tm = tmem_base;
     bool ok = true;
     int issued = 0;  // (loader) chunks whose loads are issued
+    if (warp >= kIssuerS) fewer_registers<kRegRest>();  // (the four warps together)
 
     if (warp < 8) {
         // ------------------------------------------------------------------
@@ -361,19 +367,26 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 S[c + 3] = fmaf(f.x, t.w, fmaf(f.y, t.w, S[c + 3]));
             }
         });
-        auto publish = [&] {  // S0 as bf16 pairs: this thread's 32 columns of the A operand
+        auto publish = [&](__nv_bfloat162 f) {  // 2^{-m} S0 as bf16 pairs: this thread's 32 columns of the A operand
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = pack_bf16(S[16 * q + 2 * e], S[16 * q + 2 * e + 1]);
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t y = pack_bf16(S[16 * q + 2 * e], S[16 * q + 2 * e + 1]);
+                    const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), f);  // (exact)
+                    w[e] = *reinterpret_cast<const uint32_t *>(&z);
+                }
                 tmem_st8u(tm + lane_off + kTmA + 32 * hf + 8 * q, w);
             }
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars.state);
         };
-        publish();
+        if (nch > 0) {
+            ok = warp_wait(&bars.fac[0], 0);
+            if (ok) publish(ring[0].shift);
+        }
         const int32_t kc = a.n_snap > 0 ? (int32_t)(a.snap_stride / C) : 0;  // chunks between snapshots
         const int64_t c0 = s.pos / C;
         int32_t snap_left = kc > 0 ? kc - (int32_t)(c0 % kc) : 0;
@@ -384,7 +397,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         for (int c = 0; c < nch && ok; ++c) {
             const uint32_t par = (c >> 1) & 1;
             const Factors &fac = ring[c % kRing];
-            ok = warp_wait(&bars.fac[c % kRing], (c / kRing) & 1);
+            if (c + 1 < nch) ok = warp_wait(&bars.fac[(c + 1) % kRing], ((c + 1) / kRing) & 1);  // (for its m)
             ok = ok && warp_wait(&bars.ds[c & 1], par);
             if (!ok) break;
             tc_fence_after();
@@ -415,7 +428,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             for (int m = 0; m < 2; ++m)
                 tmem_ld_frag32(tm + lane_off + ((uint32_t)(16 * m) << 16) + kTmO + 32 * hf, x[m]);
             tmem_wait_ld();
-            publish();  // S of the next chunk; O is read too
+            if (c + 1 < nch) publish(ring[(c + 1) % kRing].shift);  // S of the next chunk; O is read too
             // o = scale 2^G O, rounded, turned from channel rows to token rows
             if (c > 1) ok = warp_wait(&bars.out_empty[c & 1], par ^ 1);
             if (!ok) break;
@@ -566,7 +579,6 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_arrive(&bars.p[c & 1]);
         }
     } else if (warp == kIssuerS) {
-        fewer_registers<kRegRest>();
         // ------------------------------------------------------------------
         // MMAs of dS
         // ------------------------------------------------------------------
@@ -585,7 +597,6 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mma_commit_warp(&bars.empty[c % kStages]);
         }
     } else if (warp == kIssuerO) {
-        fewer_registers<kRegRest>();
         // ------------------------------------------------------------------
         // MMAs of QK, a chunk ahead, and of O
         // ------------------------------------------------------------------
@@ -623,7 +634,6 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mma_commit_warp(&bars.empty[c % kStages]);
         }
     } else if (warp == kStorer) {
-        fewer_registers<kRegRest>();
         const int32_t hv = (int32_t)h;
         for (int c = 0; c < nch && ok; ++c) {
             ok = warp_wait(&bars.out_full[c & 1], (c >> 1) & 1);
@@ -651,7 +661,6 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
-        fewer_registers<kRegRest>();
         // ------------------------------------------------------------------
         // Loads, and the gates' factors, two tokens per lane
         // ------------------------------------------------------------------
@@ -707,12 +716,14 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             scan_gates(g.x, g.y, lane, G, after, total);
             const bool far = !(total > kFarDecay);
             *reinterpret_cast<float2 *>(&fac.G[2 * lane]) = G;
-            *reinterpret_cast<float2 *>(&fac.f[2 * lane]) = make_float2(ex2(-G.x), ex2(-G.y));
+            const float m = far ? 0.f : rintf(-0.5f * total);
+            *reinterpret_cast<float2 *>(&fac.f[2 * lane]) = make_float2(ex2(-m - G.x), ex2(-m - G.y));
             *reinterpret_cast<float2 *>(&fac.w[2 * lane]) = make_float2(ex2(after.x), ex2(after.y));
             *reinterpret_cast<float2 *>(&fac.e[2 * lane]) =
-                far ? make_float2(1.f, 1.f) : make_float2(a.scale * ex2(G.x), a.scale * ex2(G.y));
+                far ? make_float2(1.f, 1.f) : make_float2(a.scale * ex2(m + G.x), a.scale * ex2(m + G.y));
             if (lane == 0) {
                 fac.far = far;
+                fac.shift = __float2bfloat162_rn(ex2(-m));
                 fac.decay = !fixed ? make_float2(ex2(total), 0.f)
                                    : (left >= C ? fixed_decay
                                                 : exp2_pair(gate2_exact(a.g[h]) * (double)left));

@@ -30,10 +30,12 @@ enum { GDN_GATE_CONST = 2 };
  * with S a d_v x d_k fp32 state per sequence and value head, in the state layout of
  * gdn.h.  d->gate is GDN_GATE_HEAD (log_gate (B, T, H): a decay per head and token)
  * or GDN_GATE_CONST (log_gate (H)); GDN_GATE_CHANNEL is GDN_ERR_UNSUPPORTED.
- * log_gate holds values <= 0 (0: no decay; -105 or less, -infinity too: the state is erased); sizes, dtypes, shared query/key
- * heads and alignment as in gdn.h.  q, k and v hold finite values: a value that is
+ * log_gate holds values <= 0 (0: no decay; -105 or less, -infinity too: the state is
+ * erased); sizes, dtypes, shared query/key heads and alignment as in gdn.h.  q, k and v
+ * hold finite values: a value that is
  * not finite makes the outputs of its 64-token chunk and of everything after it in
- * its sequence and head unspecified (other sequences and heads are not affected).
+ * its sequence and head unspecified (other sequences and heads are not affected), and so
+ * do sums of |q . k| |v| over a chunk of 2^67 or more (bf16, 128-wide heads).
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace gdn_linattn_chunk_fwd needs for d->T tokens in num_seqs

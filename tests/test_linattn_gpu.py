@@ -123,6 +123,18 @@ def test_chunk_strong_decays_and_resets(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("log2_decay", [-40.0, -61.0, -95.0, -99.0, -101.0, -119.0, -121.0])
+def test_chunk_large_values_under_strong_decays(dtype, log2_decay):
+    """Queries, keys and values that no norm holds down, while a chunk's decay takes a good part of the
+    exponent's range: factors of one side alone (2^99) would carry the products past it.  Sums of q k v
+    are 2^26 2^14 2^6 here."""
+    x = _inputs(1, 200, 2, 1, 128, 128, dtype, seed=19)
+    x["q"], x["k"], x["v"] = x["q"] * 3000, x["k"] * 3000, x["v"] * 10000
+    x["g"][:] = log2_decay * float(np.log(2.0)) / 64
+    _check(x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("erase", [torch.finfo(torch.float32).min, float("-inf"), -106.0])
 @pytest.mark.parametrize("T", [200, 3000])
 def test_chunk_gates_of_the_lowest_value(dtype, erase, T):
