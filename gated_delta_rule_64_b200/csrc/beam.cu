@@ -347,7 +347,8 @@ gdn_beam_join(const float *__restrict__ scores, int W, int V, int K, int nsl, in
     most = fmaxf(most, red_a[0]);
     // (0: a warp with fewer candidates than its share: all of them are wanted)
     const float bound = bits > 0 ? value_of(bits) : -INFINITY;
-    const float least = bound > -INFINITY ? bound - 4.8e-7f * (most + fabsf(bound)) : bound;  // 2 err, err <= 2^-22 of the terms
+    float least = bound - 4.8e-7f * (most + fabsf(bound));  // 2 err, err <= 2^-22 of the terms
+    if (!(least > -INFINITY)) least = -INFINITY;            // (terms past the range: nothing is sifted out)
     if (w < W) {
 #pragma unroll 4
         for (int k = 0; k < turns; ++k) {
@@ -355,7 +356,7 @@ gdn_beam_join(const float *__restrict__ scores, int W, int V, int K, int nsl, in
             if (r >= per) continue;
             bool any;
             const float x = approx(r, any);
-            if (any && x >= least) {
+            if (any && !(x < least)) {  // (a NaN, an infinite term less one, is kept)
                 const int at = atomicAdd(&s_count, 1);
                 if (at < kCap) {
                     const unsigned long long kx = dead ? 0ull : mine[r];

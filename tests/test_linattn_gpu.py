@@ -438,6 +438,19 @@ def test_beam_ties_masks_and_dead_beams(dtype):
         _beam_check(x, s, K)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [20, 1000, 9000])
+def test_beam_scores_past_the_fp32_range_in_between(dtype, V):
+    """A beam whose score less its normaliser passes the range (its continuations' scores do not), beside
+    an ordinary one, with masked places that have to fill the last ranks."""
+    x = torch.full((3, 2, V), torch.finfo(dtype).min, dtype=dtype)
+    x[1:, 1] = torch.linspace(-2, 2, V).to(dtype)
+    x[2, :, 5:] = float("-inf")
+    s = torch.tensor([[3e38, 2e38], [3e38, -1.0], [3e38, -1.0]])
+    for K in (1, 8, 33):
+        _beam_check(x, s, K)
+
+
 def test_beam_first_step_and_strided_vocabulary():
     """All beams alike (the first step after a prompt): equal scores over beams, the first beam's come first;
     logits cut from rows of a padded vocabulary whose padding holds large values."""
