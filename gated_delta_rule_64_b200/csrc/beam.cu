@@ -85,6 +85,7 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
     __shared__ uint32_t red_t[kWarps];
     __shared__ unsigned long long s_bound;
     __shared__ int s_count;
+    let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / nsl;
     const int i0 = (int)(blockIdx.x % nsl) * (kThreads * EACH);
@@ -279,6 +280,7 @@ gdn_beam_join(const float *__restrict__ scores, int W, int V, int K, int nsl, in
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t b = blockIdx.x;
     if (tid == 0) s_count = 0;
+    wait_for_previous();
     for (int w = warp; w < W; w += kWarps) {
         const SliceHead *hd = heads + (b * W + w) * nsl;
         float m = -INFINITY;
@@ -481,8 +483,8 @@ gdn_status launch_beam_select(const gdn_beam_desc &d, const void *logits, const 
         LaunchScope ls("gdn_beam_join", s);
         int lanes = kThreads;
         while (lanes * d.W > kThreads) lanes /= 2;
-        gdn_beam_join<<<(unsigned)d.B, kThreads, 0, s>>>(scores, d.W, d.V, d.K, nsl, lanes, heads, keys, out_scores,
-                                                        out_parent, out_token);
+        launch_kernel(gdn_beam_join, dim3((unsigned)d.B), dim3(kThreads), 0, s, true, scores, d.W, d.V, d.K, nsl, lanes,
+                      heads, keys, out_scores, out_parent, out_token);
     }
     return check_launch("gdn_beam_join");
 }
