@@ -27,7 +27,7 @@ static gdn_status check_lin_desc(const gdn_desc *d) {
 // a third of a block's fair share of all tokens (the tail of uneven blocks stays within
 // a third), at least 16 chunks.
 // A chunk step of the CUDA-core kernels is five times as long, so for these the start and the
-// launches weigh less: 256 fp32 tokens of 2 heads took 37 us in one segment, 24 us in four.
+// launches weigh less: 256 fp32 tokens of 2 heads took 42 us in one segment, 30 us in four.
 static int64_t choose_seg(int64_t N, int64_t units, int64_t T, int64_t rows, bool packed, int64_t wide, bool tc) {
     const double kStart = tc ? 4.0 : 0.5, kLaunch = tc ? 6.0 : 0.75;
     const int64_t kLeast = tc ? 4 : 1;
@@ -90,14 +90,15 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
     }
     // Parts of a segment's state (tensor cores), of four chunks or more and kMaxPart tokens or
     // fewer.  With a fixed gate a block sees at once whether its part reaches the segment's
-    // end, and heads whose state lasts work side by side: eight parts (long sequence of the
-    // benchmark: 505 us with one part, 142 us with eight).  With a gate per token it has to
-    // add up the gates behind its part first, 3 us even where it then has nothing to do, at
-    // one block per SM: about two blocks per SM in all (prefill: 35 us with eight parts, 16 us
-    // with two).  The CUDA-core state kernel takes a segment whole (it has d_v / 32 blocks for
-    // it already).
+    // end, and heads whose state lasts work side by side: four parts (262,144 tokens of 16
+    // heads, state and output kernel: 181 + 759 us with one part, 121 + 779 with four, 114 +
+    // 808 with eight, which the output kernel's blocks have to add up).  With a gate per token
+    // it has to add up the gates behind its part first, 3 us even where it then has nothing to
+    // do, at one block per SM: about two blocks per SM in all (4 x 4,096 tokens of 16 heads: 32
+    // us with eight parts, 19 with two).  The CUDA-core state kernel takes a segment whole (it
+    // has d_v / 32 blocks for it already).
     const int64_t chunks = p.seg / kChunk, least = (p.seg + kMaxPart - 1) / kMaxPart;
-    int64_t parts = p.fixed_gate ? 8 : (p.sslots > 0 ? 2 * sms / (p.sslots * p.H) : 1);
+    int64_t parts = p.fixed_gate ? 4 : (p.sslots > 0 ? 2 * sms / (p.sslots * p.H) : 1);
     if (parts > 8) parts = 8;
     if (parts > chunks / 4) parts = chunks / 4;
     if (parts < least) parts = least;

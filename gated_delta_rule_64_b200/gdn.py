@@ -10,6 +10,7 @@ Names follow the C ABI in ``include/gdn.h`` and ``include/gdn_linattn.h``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -364,8 +365,8 @@ def _where(stream, t, *others):
     for o in others:
         if o is not None and o.get_device() != dev:
             raise ValueError(f"tensors are on different devices: {t.device} and {o.device}")
-    if stream is None:
-        return dev, torch.cuda.current_stream(dev).cuda_stream
+    if stream is None:  # (without the Stream object around it: 0.1 us instead of 1.3)
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
     if stream != torch.cuda.current_stream(dev):
@@ -375,24 +376,15 @@ def _where(stream, t, *others):
     return dev, stream.cuda_stream
 
 
-class _On:
-    """The device of a call made current, and its stream too (so that what is allocated for it belongs to that
-    stream), where they are not."""
+_HERE = contextlib.nullcontext()
 
-    def __init__(self, dev, stream):
-        self._with = None
-        if stream is not None:
-            self._with = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != dev:
-            self._with = torch.cuda.device(dev)
 
-    def __enter__(self):
-        if self._with is not None:
-            self._with.__enter__()
-
-    def __exit__(self, *exc):
-        if self._with is not None:
-            self._with.__exit__(*exc)
+def _on(dev, stream):
+    """A context in which the device of a call is current, and its stream too (so that what is allocated for it
+    belongs to that stream)."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
 
 def _need(name, t, shape, dtype=None):
@@ -447,21 +439,21 @@ def gdn_linattn_chunk_fwd(q, k, v, log_gate, initial_state=None, cu_seqlens=None
         _need("snapshots", snapshots, (B, T // snapshot_stride, H, dv, dk), torch.float32)
     given = final_state if isinstance(final_state, torch.Tensor) else None
     dev, raw = _where(stream, q, k, v, log_gate, initial_state, cu_seqlens, out, given, snapshots, workspace)
-    with _On(dev, stream):
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+            out = torch.empty_like(v)
         if final_state is True:
-            final_state = torch.empty((N, H, dv, dk), dtype=torch.float32, device=q.device)
+            final_state = q.new_empty((N, H, dv, dk), dtype=torch.float32)
         elif final_state is False:
             final_state = None
         if snapshot_stride > 0 and snapshots is None:
-            snapshots = torch.empty((B, T // snapshot_stride, H, dv, dk), dtype=torch.float32, device=q.device)
+            snapshots = q.new_empty((B, T // snapshot_stride, H, dv, dk), dtype=torch.float32)
         d = make_desc(B, T, H, dk, dv, code, False, scale, Hq)
         d.gate = GDN_GATE_CONST if fixed else GDN_GATE_HEAD
         if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib, lib.gdn_linattn_workspace_size(ctypes.byref(d), int(N), ctypes.byref(n)))
-            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(max(n.value, 256), dtype=torch.uint8)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         st = lib.gdn_linattn_chunk_fwd(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
@@ -491,9 +483,9 @@ def gdn_linattn_decode_step(q, k, v, log_gate, state, *, scale=1.0, out=None, st
         raise ValueError(f"out must be a contiguous (B, 1, H, dv) tensor of {q.dtype}")
     dev, raw = _where(stream, q, k, v, log_gate, state, out)
     d = GdnDesc(B, 1, H, dk, dv, code, GDN_GATE_CONST if fixed else GDN_GATE_HEAD, scale, hk if hk != H else 0)
-    with _On(dev, stream):
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((B, 1, H, dv), dtype=q.dtype, device=q.device)
+            out = torch.empty_like(v) if v.dim() == 4 else v.new_empty((B, 1, H, dv))
         st = lib.gdn_linattn_decode_step(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
                                          state.data_ptr(), out.data_ptr(), raw)
     if st != GDN_OK:
@@ -547,11 +539,11 @@ def gdn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, *,
     dev, raw = _where(stream, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     d = GdnQkRopeDesc(B * T, hq, hk, dim, rot, 1 if interleaved else 0, code, _token_rows("q", q),
                       _token_rows("k", k) if hk else 0, float(eps), float(weight_offset))
-    with _On(dev, stream):
+    with _on(dev, stream):
         if q_out is None:
-            q_out = torch.empty((B, T, hq, dim), dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if k_out is None:
-            k_out = torch.empty((B, T, hk, dim), dtype=q.dtype, device=q.device)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         st = lib.gdn_qk_norm_rope(ctypes.byref(d), q.data_ptr(), k.data_ptr(), _addr(positions), _addr(inv_freq),
                                   _addr(q_weight), _addr(k_weight), q_out.data_ptr(), k_out.data_ptr(), raw)
     if st != GDN_OK:
@@ -582,17 +574,17 @@ def gdn_beam_select(logits, scores, K, *, out_scores=None, out_parent=None, out_
             _need(name, t, (B, K), dt)
     dev, raw = _where(stream, logits, scores, out_scores, out_parent, out_token, workspace)
     d = GdnBeamDesc(B, W, V, int(K), code, stride)
-    with _On(dev, stream):
+    with _on(dev, stream):
         if out_scores is None:
-            out_scores = torch.empty((B, K), dtype=torch.float32, device=logits.device)
+            out_scores = logits.new_empty((B, K), dtype=torch.float32)
         if out_parent is None:
-            out_parent = torch.empty((B, K), dtype=torch.int32, device=logits.device)
+            out_parent = logits.new_empty((B, K), dtype=torch.int32)
         if out_token is None:
-            out_token = torch.empty((B, K), dtype=torch.int32, device=logits.device)
+            out_token = torch.empty_like(out_parent)
         if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib, lib.gdn_beam_workspace_size(ctypes.byref(d), ctypes.byref(n)))
-            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=logits.device)
+            workspace = logits.new_empty(max(n.value, 256), dtype=torch.uint8)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         st = lib.gdn_beam_select(ctypes.byref(d), logits.data_ptr(), _addr(scores), out_scores.data_ptr(),
@@ -615,7 +607,7 @@ def gdn_state_reorder(state, parent, *, stream=None):
         raise ValueError(f"state must be contiguous with {B * W} rows")
     row_bytes = state.numel() // max(B * W, 1) * state.element_size()
     dev, raw = _where(stream, state, parent)
-    with _On(dev, None):
+    with _on(dev, None):
         st = lib.gdn_state_reorder(state.data_ptr(), parent.data_ptr(), B, W, row_bytes, raw)
     if st != GDN_OK:
         _check(lib, st)
