@@ -17,9 +17,14 @@
 // falls back on the K-th best of the threads' (value, index) pairs, of which at most K
 // threads have one, and the join on K rounds of a block-wide maximum.
 //
+// Measured: 32 requests of 8 beams, 128,009 bf16 logits, K = 16: 39 us.  The first kernel takes
+// 27 us, bound by its instructions (17 for each logit; the 66 MB alone are 10 us of HBM), the
+// second 18 us, a chain of dependent steps by 32 blocks, its start hidden behind the first.
+//
 // Reordering.  A thread owns 16 bytes of every beam's row of one request: it reads the
 // parents' bytes of all beams that change, then writes them, so the move is in place
-// without a second buffer and rows that stay are neither read nor written.
+// without a second buffer and rows that stay are neither read nor written.  Measured: 256 states
+// of 2 MB, most of which change: 129 us, 0.80 GB at 6.2 TB/s (0.95 of a plain copy).
 #include "linattn.cuh"
 #include "sm100.cuh"
 
@@ -438,8 +443,8 @@ gdn_state_reorder_kernel(uint4 *__restrict__ state, const int32_t *__restrict__ 
         if (w < W && s_parent[w] != w) base[w * cols] = x[w];
 }
 
-// Logits of a thread: 32, or 8 where slices of 8192 would leave SMs without one (both measured
-// on 4 beams of 32,000: 16 blocks against 64).
+// Logits of a thread: 32, or 8 where slices of 8192 would leave SMs without one (4 beams of
+// 32,000: 23 us with 16 blocks, 19 with 64, of which the join takes 15 and 10).
 int each(const gdn_beam_desc &d) {
     const int64_t big = (int64_t)d.B * d.W * ((d.V + kThreads * kEachMost - 1) / (kThreads * kEachMost));
     return big >= 148 ? kEachMost : 8;

@@ -1,8 +1,9 @@
 // Norm of every query and key head and the position rotation, in one pass.
 //
-// Bound by HBM bandwidth: every value is read once and written once (4 bytes a value
-// in bf16), and by the instructions around that: about 60 per 512 bytes read.  A group of lanes
-// holds one head of one token, two quads of four channels a lane.  Where channels i and
+// Every value is read once and written once (4 bytes a value in bf16); bound by the latency of
+// HBM at 32 warps per SM.  Measured: 16,384 tokens of 16 + 16 heads, 128 wide, 57 us, 269 MB at
+// 4.7 TB/s (0.72 of a plain copy).  A group of lanes holds one head of one token, two quads of
+// four channels a lane.  Where channels i and
 // i + rot / 2 rotate together, the quads of a lane are such partners, so the rotation needs
 // no exchange between lanes; the unrotated channels behind them, and the neighbours 2 i,
 // 2 i + 1 of the interleaved form, come as two adjacent quads.  (With eight consecutive
@@ -177,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
 template <int D>
 gdn_status launch_d(const gdn_qk_rope_desc &d, RopeArgs &a, cudaStream_t s) {
     // Tokens of a block: eight heads to a group of lanes (the angles and weights are then a
-    // small part of its work), fewer where the tokens would not fill the GPU twice.
+    // small part of its work: 57 us for the shape above, 62 with a token a block), fewer where
+    // the tokens would not fill the GPU twice.
     constexpr int kGroups = kThreads / (D / 8);
     const int heads = a.hq + a.hk;
     int tokens = 1;
