@@ -17,9 +17,10 @@
 // falls back on the K-th best of the threads' (value, index) pairs, of which at most K
 // threads have one, and the join on K rounds of a block-wide maximum.
 //
-// Measured: 32 requests of 8 beams, 128,009 bf16 logits, K = 16: 39 us.  The first kernel takes
-// 27 us, bound by its instructions (17 for each logit; the 66 MB alone are 10 us of HBM), the
-// second 18 us, a chain of dependent steps by 32 blocks, its start hidden behind the first.
+// Measured: 32 requests of 8 beams, 128,009 bf16 logits, K = 16: 35 us.  The first kernel takes
+// 25 us (the 66 MB alone are 10 us of HBM): each block's chain of load, maximum, bound and search,
+// and its instructions.  The second takes 14 us, a chain of dependent steps by 32 blocks, its
+// start hidden behind the first.
 //
 // Reordering.  A thread owns 16 bytes of every beam's row of one request: it reads the
 // parents' bytes of all beams that change, then writes them, so the move is in place
@@ -34,7 +35,6 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxK = 64;
-constexpr int kEachMost = 32;  // logits of a thread of the first kernel: 32, or 8 where that leaves SMs idle
 
 // A value's bits, ordered as unsigned integers; NaN counts as -infinity.
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -85,7 +85,7 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
                 unsigned long long *__restrict__ keys) {
     constexpr int kCap = 256;  // values at or above the bound before the fallback
     __shared__ unsigned long long best[kThreads];
-    __shared__ unsigned long long found[kMaxK * kEachMost];
+    __shared__ unsigned long long found[kMaxK * EACH > kCap ? kMaxK * EACH : kCap];
     __shared__ float red_m[kWarps], red_s[kWarps];
     __shared__ uint32_t red_t[kWarps];
     __shared__ unsigned long long s_bound;
@@ -180,25 +180,32 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
         // which of this thread's logits reach the bound (few threads have any): a bit each, then
         // those are read once more
         const float least = bound > 0 ? value_of(bound) : -INFINITY;  // (0: a warp with fewer than its share)
-        uint32_t bits = 0;  // fp32: bit e for logit e; bf16: bit e for logit 2 e, bit 16 + e for 2 e + 1
+        // fp32: bit e for logit e; bf16: bit e for logit 2 e, bit 16 + e for 2 e + 1, of 32 logits
+        constexpr int kPart = EACH < 32 ? EACH : 32;
         auto logit_of = [](int bit) { return kVec == 4 ? bit : 2 * (bit & 15) + (bit >> 4); };
-        if (kVec == 4) {
 #pragma unroll
-            for (int e = 0; e < EACH; ++e) bits |= x(e) >= least ? 1u << e : 0u;
-        } else {  // (the bound is one of the values: exact in bf16)
-            const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(raw);
-            const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
+        for (int e0 = 0; e0 < EACH; e0 += kPart) {
+            uint32_t bits = 0;
+            if (kVec == 4) {
 #pragma unroll
-            for (int e = 0; e < EACH / 2; ++e) bits |= __hge2_mask(y[e], l2) & (0x00010001u << e);
-        }
-        if (left < kThreads * EACH)
-            for (uint32_t rest = bits; rest; rest &= rest - 1) {
-                const int bit = __ffs(rest) - 1;
-                if (index_of(logit_of(bit)) >= V) bits &= ~(1u << bit);
+                for (int e = 0; e < kPart; ++e) bits |= x(e0 + e) >= least ? 1u << e : 0u;
+            } else {  // (the bound is one of the values: exact in bf16)
+                const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(raw) + e0 / 2;
+                const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
+#pragma unroll
+                for (int e = 0; e < kPart / 2; ++e) bits |= __hge2_mask(y[e], l2) & (0x00010001u << e);
             }
-        int at = atomicAdd(&s_count, __popc(bits));
-        for (; bits; bits &= bits - 1, ++at)
-            if (at < kCap) found[at] = key_at(index_of(logit_of(__ffs(bits) - 1)));
+            if (left < kThreads * EACH)
+                for (uint32_t rest = bits; rest; rest &= rest - 1) {
+                    const int bit = __ffs(rest) - 1;
+                    if (index_of(e0 + logit_of(bit)) >= V) bits &= ~(1u << bit);
+                }
+            if (bits) {
+                int at = atomicAdd(&s_count, __popc(bits));
+                for (; bits; bits &= bits - 1, ++at)
+                    if (at < kCap) found[at] = key_at(index_of(e0 + logit_of(__ffs(bits) - 1)));
+            }
+        }
     }
     if (warp == kWarps - 1) {  // the slice's maximum and sum, a warp's part per lane
         const float wm8 = lane < kWarps ? red_m[lane] : -INFINITY;
@@ -444,21 +451,24 @@ gdn_state_reorder_kernel(uint4 *__restrict__ state, const int32_t *__restrict__ 
 }
 
 // Logits of a thread: 32, or 8 where slices of 8192 would leave SMs without one (4 beams of
-// 32,000: 23 us with 16 blocks, 19 with 64, of which the join takes 15 and 10).
+// 32,000: 23 us with 16 blocks, 19 with 64, of which the join takes 15 and 10), or 64 in bf16
+// where that still gives every SM four blocks (256 beams of 128,009: 35 us a call against 39, of
+// which the join, with half the candidates, gives two).
 int each(const gdn_beam_desc &d) {
-    const int64_t big = (int64_t)d.B * d.W * ((d.V + kThreads * kEachMost - 1) / (kThreads * kEachMost));
-    return big >= 148 ? kEachMost : 8;
+    const int64_t rows = d.B * d.W;
+    auto blocks = [&](int e) { return rows * ((d.V + kThreads * e - 1) / (kThreads * e)); };
+    if (d.dtype == GDN_BF16 && blocks(64) >= 4 * 148) return 64;
+    return blocks(32) >= 148 ? 32 : 8;
 }
 int slices(const gdn_beam_desc &d) { return (d.V + kThreads * each(d) - 1) / (kThreads * each(d)); }
 
 template <typename Tin>
 void launch_slices(const gdn_beam_desc &d, const void *logits, int nsl, SliceHead *heads, unsigned long long *keys,
                    cudaStream_t s) {
-    const unsigned n = (unsigned)(d.B * d.W * nsl);
-    if (each(d) == kEachMost)
-        gdn_beam_slices<Tin, kEachMost><<<n, kThreads, 0, s>>>((const Tin *)logits, d.row_stride, d.V, d.K, nsl, heads, keys);
-    else
-        gdn_beam_slices<Tin, 8><<<n, kThreads, 0, s>>>((const Tin *)logits, d.row_stride, d.V, d.K, nsl, heads, keys);
+    constexpr int kMost = sizeof(Tin) == 2 ? 64 : 32;
+    const int e = each(d);
+    auto kern = e == 8 ? gdn_beam_slices<Tin, 8> : e == 32 ? gdn_beam_slices<Tin, 32> : gdn_beam_slices<Tin, kMost>;
+    kern<<<(unsigned)(d.B * d.W * nsl), kThreads, 0, s>>>((const Tin *)logits, d.row_stride, d.V, d.K, nsl, heads, keys);
 }
 
 }  // namespace

@@ -451,6 +451,25 @@ def test_beam_scores_past_the_fp32_range_in_between(dtype, V):
         _beam_check(x, s, K)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,V", [(40, 9001), (80, 16500)])
+def test_beam_many_requests(dtype, B, V):
+    """Enough beams for the larger slices; among them runs of equal values, masks, sorted logits, dead beams."""
+    rng = np.random.default_rng(B)
+    x = torch.from_numpy(rng.normal(0, 2, size=(B, 8, V)).astype(np.float32))
+    x[1] = 0.0
+    x[2] = float("-inf")
+    x[2, 3, V - 1] = 1.0
+    x[3] = torch.arange(V) / V
+    x[4] = -torch.arange(V) / V
+    x[5, :, 64:] = torch.finfo(dtype).min
+    x[6, 2, 17], x[6, 3, 18] = float("nan"), float("inf")
+    x[7] = torch.round(x[7])
+    s = torch.from_numpy(-5 * rng.random((B, 8), dtype=np.float32))
+    for K in (1, 16, 64):
+        _beam_check(x.to(dtype), s, K)
+
+
 def test_beam_first_step_and_strided_vocabulary():
     """All beams alike (the first step after a prompt): equal scores over beams, the first beam's come first;
     logits cut from rows of a padded vocabulary whose padding holds large values."""
