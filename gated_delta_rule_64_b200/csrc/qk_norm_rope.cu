@@ -1,8 +1,9 @@
 // Norm of every query and key head and the position rotation, in one pass.
 //
 // Every value is read once and written once (4 bytes a value in bf16); bound by the latency of
-// HBM at 32 warps per SM.  Measured: 16,384 tokens of 16 + 16 heads, 128 wide, 57 us, 269 MB at
-// 4.7 TB/s (0.72 of a plain copy).  A group of lanes holds one head of one token, two quads of
+// HBM at 32 warps per SM, so three heads of each group are on their way (with two: 56 us; fp32,
+// of twice the bytes, keeps its registers with six blocks per SM).  Measured: 16,384 tokens of
+// 16 + 16 heads, 128 wide, 54 us, 269 MB at 5.0 TB/s (0.76 of a plain copy).  A group of lanes holds one head of one token, two quads of
 // four channels a lane.  Where channels i and
 // i + rot / 2 rotate together, the quads of a lane are such partners, so the rotation needs
 // no exchange between lanes; the unrotated channels behind them, and the neighbours 2 i,
@@ -65,7 +66,7 @@ struct RopeArgs {
 };
 
 template <int D, typename Tin, bool INTER>
-__global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 8 : 6) gdn_qk_norm_rope_kernel(const RopeArgs a) {
     constexpr int kGroup = D / 8;               // lanes of a head
     constexpr int kGroups = kThreads / kGroup;  // of a block; as many tokens at most
     __shared__ __align__(16) float s_cos[kGroups * D / 2], s_sin[kGroups * D / 2];
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
     const int64_t qo = (int64_t)h0 * D;
     const Tin *q = static_cast<const Tin *>(a.q) + row * a.q_stride + qo, *k = static_cast<const Tin *>(a.k) + row * a.k_stride + qo;
     const int nq = live ? (a.hq - h0 + step - 1) >> sb : 0, nk = live ? (a.hk - h0 + step - 1) >> sb : 0;  // (0 past the last head)
-    raw x0 = {}, x1 = {}, y0 = {}, y1 = {};
+    raw x0 = {}, x1 = {}, y0 = {}, y1 = {}, z0 = {}, z1 = {};
     if (nq > 0) {  // in flight while the angles are formed
         x0 = load_quad(q + c0);
         x1 = load_quad(q + c1);
@@ -94,6 +95,10 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
     if (nq > 1) {
         y0 = load_quad(q + step * D + c0);
         y1 = load_quad(q + step * D + c1);
+    }
+    if (nq > 2) {
+        z0 = load_quad(q + 2 * step * D + c0);
+        z1 = load_quad(q + 2 * step * D + c1);
     }
     if (half > 0) {  // a thread takes one frequency, of every (128 / width)-th token
         const int i = tid & ((1 << a.half_bits) - 1), stride = kThreads >> a.half_bits;
@@ -117,20 +122,22 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
                  : Quad{make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
     };
     // `n` heads of this group, of `most` that any group of the warp has (the shuffles are warp-wide);
-    // x and y hold the first two.  With the weights taken into the angles (w cos, w sin) a pair of
+    // x, y and z hold the first three.  With the weights taken into the angles (w cos, w sin) a pair of
     // partners is two multiply-adds each, and the norm one product at the end.
     auto run = [&](const Tin *src, Tin *dst, int n, int most, const float *wp) {
         const Quad w0 = weight(wp, c0), w1 = weight(wp, c1);
         const Quad cp = scale(w0, cs), cr = scale(w1, cs), sp = scale(w0, sn);
         const Quad sr = {make_float2(-w1.a.x * sn.a.x, -w1.a.y * sn.a.y), make_float2(-w1.b.x * sn.b.x, -w1.b.y * sn.b.y)};
-        const Tin *ahead = src + 2 * step * D;
+        const Tin *ahead = src + 3 * step * D;
         for (int i = 0; i < most; ++i) {
             const Quad p = unpack(x0), r = unpack(x1);
             x0 = y0;
             x1 = y1;
-            if (i + 2 < n) {
-                y0 = load_quad(ahead + c0);
-                y1 = load_quad(ahead + c1);
+            y0 = z0;
+            y1 = z1;
+            if (i + 3 < n) {
+                z0 = load_quad(ahead + c0);
+                z1 = load_quad(ahead + c1);
             }
             ahead += step * D;
             float2 s2 = mul2(p.a, p.a);
@@ -171,6 +178,10 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
             y0 = load_quad(k + step * D + c0);
             y1 = load_quad(k + step * D + c1);
         }
+        if (nk > 2) {
+            z0 = load_quad(k + 2 * step * D + c0);
+            z1 = load_quad(k + 2 * step * D + c1);
+        }
         run(k, static_cast<Tin *>(a.k_out) + row * a.hk * D + qo, nk, (a.hk + step - 1) >> sb, a.kw);
     }
 }
@@ -178,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 8) gdn_qk_norm_rope_kernel(const Rop
 template <int D>
 gdn_status launch_d(const gdn_qk_rope_desc &d, RopeArgs &a, cudaStream_t s) {
     // Tokens of a block: eight heads to a group of lanes (the angles and weights are then a
-    // small part of its work: 57 us for the shape above, 62 with a token a block), fewer where
+    // small part of its work: four heads or sixteen take 60 and 59 us), fewer where
     // the tokens would not fill the GPU twice.
     constexpr int kGroups = kThreads / (D / 8);
     const int heads = a.hq + a.hk;
