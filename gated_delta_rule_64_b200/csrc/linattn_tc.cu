@@ -309,6 +309,10 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (tid == 0) s = found;
         __syncthreads();
     }
+    // Roles that wait for the state's warps give up after a while, so none may start long before
+    // these can: a state kernel ends within a block's time, the combine kernel, which goes over all
+    // sequences, need not.
+    if (!a.chained) wait_for_previous();
     const int len = (int)s.len, nch = (len + C - 1) / C;
     const int cut = len % C ? nch - 1 : -1;  // the chunk with rows behind the segment, if any
     constexpr int kIssuerS = 16, kIssuerO = 17, kStorer = 18, kLoader = 19;
@@ -358,7 +362,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         float S[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) S[c] = 0.f;
-        wait_for_previous();  // (the other roles need nothing that earlier kernels of the call wrote)
+        wait_for_previous();  // (only here: the other roles need nothing that the state kernel wrote)
         start_state(a, s, h, (int64_t)(D * D), [&](float2 f, const float *src) {
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
