@@ -676,7 +676,8 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             prefetch_tmap(&mk);
             prefetch_tmap(&mv);
         }
-        const float gh = fixed ? gate2(a.g[h]) : 0.f;
+        // (a call without tokens may come without gates: a segment without chunks reads none)
+        const float gh = fixed && nch > 0 ? gate2(a.g[h]) : 0.f;
         // A head's gates lie H floats apart, a memory sector each: they are asked for early.
         const float *gates = a.g + (fixed ? 0 : s.start * a.H + h);
         auto ask_gates = [&](int c) {
@@ -689,7 +690,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             async_commit();  // (a group per chunk, empty or not)
         };
         for (int c = 0; c < kGateAhead; ++c) ask_gates(c);
-        const float2 fixed_decay = fixed ? exp2_pair(gate2_exact(a.g[h]) * C) : make_float2(0.f, 0.f);
+        const float2 fixed_decay = fixed && nch > 0 ? exp2_pair(gate2_exact(a.g[h]) * C) : make_float2(0.f, 0.f);
         for (int c = 0; c < nch; ++c) {
             const int stage = c % kStages;
             if (c >= kStages) ok = warp_wait(&bars.empty[stage], ((c / kStages) & 1) ^ 1);

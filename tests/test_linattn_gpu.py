@@ -9,6 +9,8 @@ Tolerances (relative L2 over a tensor), from the arithmetic:
   norm and rotation, fp32: mean square 2^-24 * 8 at most, rsqrt 2^-22, angle 2^-22 of a turn in the
     sine and cosine (1.5e-6 of the head's length at worst): 3e-6.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -210,6 +212,24 @@ def test_chunk_empty_prompt_copies_the_state(d):
     _, fin, _ = gdn.gdn_linattn_chunk_fwd(e(2, 0, 3, d), e(2, 0, 3, d), e(2, 0, 3, d),
                                           torch.zeros(3, device="cuda"))
     assert not fin.any()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128)])
+@pytest.mark.parametrize("gate", [gdn.GDN_GATE_HEAD, gdn.GDN_GATE_CONST])
+@pytest.mark.parametrize("packed", [False, True])
+def test_chunk_without_tokens_needs_no_inputs(dtype, d, gate, packed):
+    """The C entry point takes a call without tokens whose q, k, v, gates and output are NULL: the final states
+    are the initial ones."""
+    lib = gdn.load_library()
+    h0, fin = torch.randn(2, 3, d, d, device="cuda"), torch.full((2, 3, d, d), 5.0, device="cuda")
+    ws = torch.full((4096,), 255, dtype=torch.uint8, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    desc = gdn.GdnDesc(1 if packed else 2, 0, 3, d, d, gdn.GDN_F32 if dtype == "f32" else gdn.GDN_BF16, gate, 1.0, 0)
+    st = lib.gdn_linattn_chunk_fwd(ctypes.byref(desc), None, None, None, None, h0.data_ptr(),
+                                   cu.data_ptr() if packed else None, 2, 0, None, fin.data_ptr(), None,
+                                   ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == gdn.GDN_OK, lib.gdn_last_error().decode()
+    assert gdn.gdn_chunk_status(ws) == (gdn.GDN_OK, gdn.GDN_DEV_OK) and torch.equal(fin, h0)
 
 
 @pytest.mark.parametrize("cu", [[0, 90, 40, 200], [-5, 300, 7, 1000], [200, 0, 0, 0], [7, 60, 61, 100]])
