@@ -482,17 +482,21 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const Factors &fac = ring[c % kRing];
             ok = warp_wait(&bars.full[stage], (c / kStages) & 1);  // (the factors too)
             if (!ok) break;
-            if (c == cut) {  // rows behind the sequence: whatever lies there stays out of the sums
-                for (int i = tid - 256; i < 64 * 8; i += 128)
-                    if ((i >> 3) >= len % C) {
-                        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(st + kStK + i * 16) = z;
-                        *reinterpret_cast<uint4 *>(st + kStK + kHalfQK + i * 16) = z;
-                        *reinterpret_cast<uint4 *>(st + kStV + i * 16) = z;
-                        *reinterpret_cast<uint4 *>(st + kStV + kHalfV + i * 16) = z;
-                    }
+            if (c == cut) {
+                // Rows behind the sequence: whatever lies there stays out of the sums.  A warp clears
+                // the channels of V that it reads itself and a quarter of K, which only products
+                // that wait for the terms of all four warps read: no barrier among the four, at which
+                // three would stay if a wait of the fourth gave up.
+                const uint32_t z = (uint32_t)(w >> 1) * kHalfV;  // (halves of K are twice as far apart)
+                for (int i = lane; i < 64 * 4; i += 32) {
+                    const int row = i >> 2, p = (w & 1) * 4 + (i & 3);
+                    if (row < len % C) continue;
+                    const uint32_t at = row * 128 + ((p ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(st + kStV + z + at) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(st + kStK + 2 * z + at) = make_uint4(0u, 0u, 0u, 0u);
+                }
                 fence_async_smem();
-                named_bar_sync(2, 128);
+                __syncwarp();
             }
             if (c > 1) ok = warp_wait(&bars.ds[c & 1], ((c >> 1) & 1) ^ 1);  // dS of chunk c - 2 has read this buffer
             if (!ok) break;

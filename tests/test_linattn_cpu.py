@@ -108,6 +108,15 @@ def test_chunk_no_sequences_is_a_no_op(lib):
     assert _fwd(lib, _desc(B=1, T=0), cu=8, n=0, ws=None) == gdn.GDN_OK
 
 
+def test_no_barrier_over_part_of_a_block():
+    """The roles of the tensor-core kernels leave their loops where a wait gives up, each on its own.  A
+    barrier that counts some of the block's warps would hold those that reach it for good (the barrier
+    of the whole block at the kernels' ends is reached by all), so the kernels have none."""
+    text = open(os.path.join(ROOT, "gated_delta_rule_64_b200", "csrc", "linattn_tc.cu")).read()
+    code = re.sub(r"//[^\n]*", "", text)
+    assert "mbar_wait(" in code and not re.search(r"named_bar|bar\.sync|barrier\.|bar\.arrive", code)
+
+
 def test_workspace_size(lib):
     n = ctypes.c_size_t()
     size = lambda d, N: (lib.gdn_linattn_workspace_size(ctypes.byref(d), N, ctypes.byref(n)), n.value)[1]  # noqa: E731
