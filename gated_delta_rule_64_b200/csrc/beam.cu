@@ -81,7 +81,7 @@ __device__ __noinline__ unsigned long long kth_of_256(const unsigned long long *
 
 template <typename Tin, int EACH>
 __global__ void __launch_bounds__(kThreads)
-gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K, int nsl, SliceHead *__restrict__ heads,
+gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, uint32_t V, int K, int nsl, SliceHead *__restrict__ heads,
                 unsigned long long *__restrict__ keys) {
     constexpr int kCap = 256;  // values at or above the bound before the fallback
     __shared__ unsigned long long best[kThreads];
@@ -93,7 +93,8 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
     let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / nsl;
-    const int i0 = (int)(blockIdx.x % nsl) * (kThreads * EACH);
+    // (indices are unsigned: those of a last slice may pass the vocabulary, and 2^31, by a slice)
+    const uint32_t i0 = blockIdx.x % (uint32_t)nsl * (uint32_t)(kThreads * EACH);
     const Tin *p = logits + row * row_stride;
     constexpr int kVec = 16 / (int)sizeof(Tin);
     const bool wide = ((uintptr_t)(p + i0) & 15) == 0;
@@ -109,11 +110,11 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
         return __uint_as_float(e & 1 ? u[(e % 8) / 2] & 0xffff0000u : u[(e % 8) / 2] << 16);
     };
-    auto index_of = [&](int e) { return i0 + (e / kVec) * (kThreads * kVec) + tid * kVec + e % kVec; };
+    auto index_of = [&](int e) { return i0 + (uint32_t)((e / kVec) * (kThreads * kVec) + tid * kVec + e % kVec); };
     constexpr uint32_t kLow = kVec == 4 ? 0xff800000u : 0xff80ff80u;  // -infinity
 #pragma unroll
     for (int c = 0; c < EACH / kVec; ++c) {
-        const int i = index_of(c * kVec);
+        const uint32_t i = index_of(c * kVec);
         if (wide && i + kVec <= V) {
             raw[c] = __ldcs(reinterpret_cast<const uint4 *>(p + i));
         } else {
@@ -157,7 +158,7 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
     // (a thread behind the vocabulary has nothing, not even -infinity)
     const uint32_t top = index_of(0) < V ? order_bits(m) : 0u;
     // (a last slice may leave whole warps without a logit: the others' share grows)
-    const int left = V - i0, busy = left >= kThreads * kVec ? kWarps : (left + 32 * kVec - 1) / (32 * kVec);
+    const int left = (int)(V - i0), busy = left >= kThreads * kVec ? kWarps : (left + 32 * kVec - 1) / (32 * kVec);
     const uint32_t t = rth_of_warp(top, (K + busy - 1) / busy, lane);
     float wm = m;
 #pragma unroll
@@ -175,7 +176,7 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
 #pragma unroll
     for (int w = 1; w < kWarps; ++w)
         if (w < busy) bound = min(bound, red_t[w]);
-    auto key_at = [&](int i) { return ((unsigned long long)order_bits(to_f32<Tin>(p[i])) << 32) | (uint32_t)~i; };
+    auto key_at = [&](uint32_t i) { return ((unsigned long long)order_bits(to_f32<Tin>(p[i])) << 32) | ~i; };
     if (top >= bound && top > 0) {
         // which of this thread's logits reach the bound (few threads have any): a bit each, then
         // those are read once more
@@ -225,7 +226,7 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
         unsigned long long mine = 0;
 #pragma unroll 1
         for (int e = 0; e < EACH; ++e) {
-            const int i = index_of(e);
+            const uint32_t i = index_of(e);
             const unsigned long long kx = i < V ? key_at(i) : 0ull;
             mine = kx > mine ? kx : mine;
         }
@@ -240,7 +241,7 @@ gdn_beam_slices(const Tin *__restrict__ logits, int64_t row_stride, int V, int K
         if (mine >= s_bound) {  // at most K threads
 #pragma unroll 1
             for (int e = 0; e < EACH; ++e) {
-                const int i = index_of(e);
+                const uint32_t i = index_of(e);
                 const unsigned long long kx = i < V ? key_at(i) : 0ull;
                 if (kx >= s_bound) found[atomicAdd(&s_count, 1)] = kx;
             }
@@ -450,17 +451,20 @@ gdn_state_reorder_kernel(uint4 *__restrict__ state, const int32_t *__restrict__ 
         if (w < W && s_parent[w] != w) base[w * cols] = x[w];
 }
 
+// Slices of a beam with `each` logits a thread.
+int64_t slices_of(int64_t V, int each) { return (V + kThreads * each - 1) / (kThreads * each); }
+
 // Logits of a thread: 32, or 8 where slices of 8192 would leave SMs without one (4 beams of
 // 32,000: 23 us with 16 blocks, 19 with 64, of which the join takes 15 and 10), or 64 in bf16
 // where that still gives every SM four blocks (256 beams of 128,009: 35 us a call against 39, of
 // which the join, with half the candidates, gives two).
 int each(const gdn_beam_desc &d) {
     const int64_t rows = d.B * d.W;
-    auto blocks = [&](int e) { return rows * ((d.V + kThreads * e - 1) / (kThreads * e)); };
+    auto blocks = [&](int e) { return rows * slices_of(d.V, e); };
     if (d.dtype == GDN_BF16 && blocks(64) >= 4 * 148) return 64;
     return blocks(32) >= 148 ? 32 : 8;
 }
-int slices(const gdn_beam_desc &d) { return (d.V + kThreads * each(d) - 1) / (kThreads * each(d)); }
+int slices(const gdn_beam_desc &d) { return (int)slices_of(d.V, each(d)); }
 
 template <typename Tin>
 void launch_slices(const gdn_beam_desc &d, const void *logits, int nsl, SliceHead *heads, unsigned long long *keys,
@@ -468,7 +472,7 @@ void launch_slices(const gdn_beam_desc &d, const void *logits, int nsl, SliceHea
     constexpr int kMost = sizeof(Tin) == 2 ? 64 : 32;
     const int e = each(d);
     auto kern = e == 8 ? gdn_beam_slices<Tin, 8> : e == 32 ? gdn_beam_slices<Tin, 32> : gdn_beam_slices<Tin, kMost>;
-    kern<<<(unsigned)(d.B * d.W * nsl), kThreads, 0, s>>>((const Tin *)logits, d.row_stride, d.V, d.K, nsl, heads, keys);
+    kern<<<(unsigned)(d.B * d.W * nsl), kThreads, 0, s>>>((const Tin *)logits, d.row_stride, (uint32_t)d.V, d.K, nsl, heads, keys);
 }
 
 }  // namespace

@@ -228,6 +228,17 @@ def test_beam_no_requests_is_a_no_op(lib):
     assert lib.gdn_beam_workspace_size(None, ctypes.byref(n)) == INV
 
 
+@pytest.mark.parametrize("V", [(1 << 31) - 1, (1 << 31) - 2000, (1 << 31) - 16384, (1 << 31) - 16385])
+@pytest.mark.parametrize("dtype", [gdn.GDN_F32, gdn.GDN_BF16])
+def test_beam_workspace_of_the_largest_vocabulary(lib, V, dtype):
+    """A key of 8 bytes for each of K = 8 continuations of a slice, and 8 bytes of sums: slices are 2,048
+    logits or more."""
+    n = ctypes.c_size_t()
+    d = gdn.GdnBeamDesc(1, 1, V, 8, dtype, V)
+    assert lib.gdn_beam_workspace_size(ctypes.byref(d), ctypes.byref(n)) == gdn.GDN_OK
+    assert 64 <= n.value <= (V // 2048 + 1) * 72 + 512
+
+
 def test_reorder_refusals(lib):
     def call(B=2, W=4, row=64, state=0, parent=1, so=0, po=0):
         return lib.gdn_state_reorder(_p(state, so), _p(parent, po), B, W, row, None)

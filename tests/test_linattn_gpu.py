@@ -490,6 +490,25 @@ def test_beam_many_requests(dtype, B, V):
         _beam_check(x.to(dtype), s, K)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [(1 << 31) - 1, (1 << 31) - 9000])
+def test_beam_largest_vocabulary(dtype, V):
+    """W V = 2^31 - 1, the most that one request may have: indices of the last slice pass the vocabulary's end
+    and 2^31.  All logits but three are 0, so the normaliser is log(V - 3 + the three's exponentials); it is
+    good to 2^-17, and the scores near -21 to half an fp32 step, 2^-20."""
+    x = torch.zeros(1, 1, V, dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
+    peaks = {V - 1: 3.0, (1 << 30) + 5: 2.5, 7: 2.0}
+    for i, y in peaks.items():
+        x[0, 0, i] = y
+    score, parent, token = gdn.gdn_beam_select(x, None, 8)
+    assert token[0].tolist() == [V - 1, (1 << 30) + 5, 7, 0, 1, 2, 3, 4] and not parent.any()
+    lse = np.log(V - 3 + sum(np.exp(y) for y in peaks.values()))
+    want = np.array([3.0, 2.5, 2.0] + [0.0] * 5) - lse
+    assert np.abs(score[0].cpu().double().numpy() - want).max() <= 2.0 ** -17 + 2.0 ** -20
+    del x
+    torch.cuda.empty_cache()
+
+
 def test_beam_first_step_and_strided_vocabulary():
     """All beams alike (the first step after a prompt): equal scores over beams, the first beam's come first;
     logits cut from rows of a padded vocabulary whose padding holds large values."""

@@ -18,3 +18,15 @@ def test_linattn_host_code_under_sanitizers():
         subprocess.run([gdn_build.nvcc(), *gdn_build.ARCH, *objs, mobj, "-o", exe,
                         *[a for f in base.SAN for a in ("-Xcompiler", f)]], check=True)
     assert "0 failures" in base._run(exe, ASAN_OPTIONS="detect_leaks=0:protect_shadow_gap=0")
+
+
+def test_linattn_limits_under_sanitizers():
+    base.test_library_host_code_under_sanitizers()
+    main = os.path.join(base.HERE, "csrc", "linattn_limits_main.c")
+    exe, mobj = os.path.join(base.OUT, "linattn_limits"), os.path.join(base.OUT, "linattn_limits_main.o")
+    if base._stale(exe, gdn_build.deps() + [main]):
+        objs = [os.path.join(base.OUT, os.path.basename(src) + ".o") for src in gdn_build.sources()]
+        subprocess.run(["gcc", *base.SAN, "-g", "-I", gdn_build.INCLUDE, "-c", main, "-o", mobj], check=True)
+        subprocess.run([gdn_build.nvcc(), *gdn_build.ARCH, *objs, mobj, "-o", exe,
+                        *[a for f in base.SAN for a in ("-Xcompiler", f)]], check=True)
+    assert "0 failures" in base._run(exe, ASAN_OPTIONS="detect_leaks=0:protect_shadow_gap=0")
