@@ -223,7 +223,7 @@ gdn_status gdn_linattn_chunk_fwd(const gdn_desc *d, const void *q, const void *k
     a.part_len = p.part_len;
     // (blocks that add up their start states read the initial state while others may already write
     // the final one)
-    a.chained = p.chained && final_state != initial_state;
+    a.chained = p.chained && !(final_state && final_state == initial_state);
     a.scale = d->scale;
     a.snap_stride = snapshot_stride;
     a.n_snap = n_snap;

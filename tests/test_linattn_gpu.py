@@ -202,6 +202,26 @@ def test_chunk_long_in_place_split(dtype, d, decay):
     assert rel_l2(state, f) <= TOL_F32
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+@pytest.mark.parametrize("h0,final,combined", [(False, "none", False), (True, "none", False), (False, "new", False),
+                                               (True, "new", False), (True, "initial", True)])
+def test_chunk_split_start_states(dtype, d, h0, final, combined):
+    """A split sequence's blocks add up their start states themselves, with or without an initial and a final
+    state; the combine kernel runs where the final state replaces the initial one."""
+    x = _inputs(1, 6000, 2, 1, d, d, dtype, seed=22, h0=h0, decay=0.02)
+    p = [x[n].cuda() for n in "qkvg"] + [x["h0"].cuda() if h0 else None]
+    gdn.profile_read()
+    gdn.profile_enable(True)
+    out, fin, _ = gdn.gdn_linattn_chunk_fwd(*p, final_state={"none": None, "new": True, "initial": p[4]}[final])
+    gdn.profile_enable(False)
+    names = gdn.profile_read()
+    assert any("state" in n for n in names), names  # split
+    assert ("gdn_linattn_combine" in names) == combined, names
+    o, f, _ = L.linear_attention(x["q"], x["k"], x["v"], x["g"], x["h0"])
+    assert rel_l2(out, o) <= (TOL_F32 if dtype == "f32" else TOL_BF16)
+    assert fin is None or rel_l2(fin, f) <= TOL_F32
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_chunk_empty_prompt_copies_the_state(d):
     h0 = torch.randn(2, 3, d, d, device="cuda")
