@@ -282,7 +282,9 @@ gdn_status gdn_qk_norm_rope(const gdn_qk_rope_desc *d, const void *q, const void
     if (d->rows == 0) return GDN_OK;
     if (d->q_stride < qrow || d->q_stride % vec != 0 || (d->hk > 0 && (d->k_stride < krow || d->k_stride % vec != 0)))
         return fail(GDN_ERR_INVALID_ARG, "strides must hold a token's heads and be multiples of 16 bytes");
-    if (d->q_stride > (1LL << 40) || d->k_stride > (1LL << 40)) return fail(GDN_ERR_INVALID_ARG, "stride too large");
+    // (offsets in elements and bytes stay well inside int64, as in check_desc)
+    if ((double)d->rows * (double)d->q_stride > 4.0e15 || (d->hk > 0 && (double)d->rows * (double)d->k_stride > 4.0e15))
+        return fail(GDN_ERR_INVALID_ARG, "stride too large");
     if (!q || !q_out || (d->hk > 0 && (!k || !k_out)) || (d->rot > 0 && (!positions || !inv_freq)))
         return fail(GDN_ERR_INVALID_ARG, "q, k, their outputs, and (with rot > 0) positions and inv_freq are required");
     if (!aligned16(q) || !aligned16(q_out) || (d->hk > 0 && (!aligned16(k) || !aligned16(k_out))))
@@ -321,9 +323,10 @@ static gdn_status check_beam_desc(const gdn_beam_desc *d) {
     if (d->K < 1 || d->K > 64 || d->K > wv)
         return fail(GDN_ERR_INVALID_ARG, "need 1 <= K <= min(64, W V) (got %d)", d->K);
     if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return fail(GDN_ERR_INVALID_ARG, "unknown dtype %d", d->dtype);
-    if (d->row_stride < d->V || d->row_stride > (1LL << 40))
-        return fail(GDN_ERR_INVALID_ARG, "row_stride must be at least V");
+    if (d->row_stride < d->V) return fail(GDN_ERR_INVALID_ARG, "row_stride must be at least V");
     if (d->B > 0x7fffffffLL / d->W) return fail(GDN_ERR_UNSUPPORTED, "more than 2^31 - 1 beams");
+    if (d->row_stride > (1LL << 40) || (double)d->B * d->W * (double)d->row_stride > 4.0e15)
+        return fail(GDN_ERR_INVALID_ARG, "row_stride too large");
     return GDN_OK;
 }
 

@@ -23,7 +23,27 @@ static void beam_vocabulary(int32_t V, int32_t K, int32_t dtype) {
     EXPECT(n >= (size_t)K * 8 && n <= ((size_t)V / 2048 + 1) * ((size_t)K * 8 + 8) + 512);
 }
 
+#define P(i) ((void *)(uintptr_t)((1ULL << 40) + (uint64_t)(i) * (1ULL << 36)))
+
+/* Rows times a stride that no buffer can have (2^70 elements) are refused before they are multiplied. */
+static void far_rows(int64_t stride) {
+    gdn_qk_rope_desc r = {0x7fffffffLL, 4, 2, 128, 64, 0, GDN_F32, stride, 256, 1e-6f, 0.f};
+    EXPECT(gdn_qk_norm_rope(&r, P(0), P(1), P(2), P(3), P(4), P(5), P(6), P(7), NULL) == GDN_ERR_INVALID_ARG);
+    r.q_stride = 512;
+    r.k_stride = stride;
+    EXPECT(gdn_qk_norm_rope(&r, P(0), P(1), P(2), P(3), P(4), P(5), P(6), P(7), NULL) == GDN_ERR_INVALID_ARG);
+    gdn_beam_desc b = {0x7fffffffLL / 64, 64, 100, 8, GDN_F32, stride};
+    size_t n = 0;
+    EXPECT(gdn_beam_workspace_size(&b, &n) == GDN_ERR_INVALID_ARG);
+    EXPECT(gdn_beam_select(&b, P(0), P(1), P(2), P(3), P(4), P(5), (size_t)1 << 60, NULL) == GDN_ERR_INVALID_ARG);
+}
+
 int main(void) {
+    far_rows(1LL << 40);
+    far_rows(1LL << 34);
+    far_rows(1LL << 62);
+    far_rows(0x7ffffffffffffff0LL);
+
     for (int32_t under = 0; under < 20000; under += 331)
         for (int32_t K = 1; K <= 64; K += 21)
             for (int32_t dt = 0; dt < 2; ++dt) beam_vocabulary(0x7fffffff - under, K, dt);
