@@ -17,6 +17,12 @@ static gdn_status check_lin_desc(const gdn_desc *d) {
     return check_desc(&c);
 }
 
+// N states in elements, and the blocks that work on them, stay well inside int64 (check_desc
+// bounds what has tokens).
+static bool states_fit(const gdn_desc &d, int64_t N) {
+    return (double)N * (double)d.H * (double)(d.dk * d.dv) <= 4.0e15;
+}
+
 // Tokens per segment (a multiple of 64; at least the longest possible sequence: no
 // split).  `units` blocks work on one segment of one sequence, `wide` blocks run at once.
 //
@@ -132,6 +138,11 @@ gdn_status gdn_linattn_workspace_size(const gdn_desc *d, int32_t num_seqs, size_
     if (st != GDN_OK) return st;
     if (!bytes) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
     if (num_seqs < 0) return fail(GDN_ERR_INVALID_ARG, "num_seqs < 0");
+    if (!states_fit(*d, num_seqs)) return fail(GDN_ERR_INVALID_ARG, "problem too large");
+    if (num_seqs == 0) {  // (nothing to plan: T may be anything)
+        *bytes = kStatusBytes;
+        return GDN_OK;
+    }
     // either gate kind; packed, and fixed-length where the number of sequences allows it
     size_t total = 0;
     for (int i = 0; i < 4; ++i) {
@@ -164,6 +175,7 @@ gdn_status gdn_linattn_chunk_fwd(const gdn_desc *d, const void *q, const void *k
     if (snapshot_stride < 0 || snapshot_stride % kChunk != 0)
         return fail(GDN_ERR_INVALID_ARG, "snapshot_stride must be 0 or a positive multiple of 64");
     const int64_t n_snap = snapshot_stride > 0 ? d->T / snapshot_stride : 0;
+    if (!states_fit(*d, N)) return fail(GDN_ERR_INVALID_ARG, "problem too large");
     const int64_t rows = d->B * d->T;
     if (rows > 0x7fffffffLL) return fail(GDN_ERR_UNSUPPORTED, "more than 2^31 - 1 token rows");
     const size_t el = d->dtype == GDN_F32 ? 4 : 2;
@@ -182,8 +194,8 @@ gdn_status gdn_linattn_chunk_fwd(const gdn_desc *d, const void *q, const void *k
         (snapshots && !aligned16(snapshots)))
         return fail(GDN_ERR_INVALID_ARG, "state pointers must be 16-byte aligned");
     if (n_snap > 0 && !snapshots) return fail(GDN_ERR_INVALID_ARG, "snapshots buffer is required");
-    const lin::Plan p = lin::make_plan(*d, N, packed);
     if (N == 0) return GDN_OK;
+    const lin::Plan p = lin::make_plan(*d, N, packed);
     if (!workspace) return fail(GDN_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", p.total);
     if (((uintptr_t)workspace & 255u) != 0) return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     if (workspace_bytes < p.total)

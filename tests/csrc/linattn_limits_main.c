@@ -38,7 +38,28 @@ static void far_rows(int64_t stride) {
     EXPECT(gdn_beam_select(&b, P(0), P(1), P(2), P(3), P(4), P(5), (size_t)1 << 60, NULL) == GDN_ERR_INVALID_ARG);
 }
 
+/* No sequences: nothing to plan, whatever the number of tokens or heads.  States past 4e15 elements are refused. */
+static void few_and_many_sequences(int32_t dtype, int32_t gate) {
+    size_t n = 0;
+    gdn_desc d = {0, 0x7fffffffffffffffLL, 16, 128, 128, dtype, gate, 1.0f, 0};
+    EXPECT(gdn_linattn_workspace_size(&d, 0, &n) == GDN_OK && n >= 4 && n <= 4096);
+    EXPECT(gdn_linattn_chunk_fwd(&d, NULL, NULL, NULL, NULL, NULL, NULL, 0, 0, NULL, NULL, NULL, NULL, 0, NULL) == GDN_OK);
+    d.T = 0;
+    d.H = 1LL << 61;
+    EXPECT(gdn_linattn_workspace_size(&d, 0, &n) == GDN_OK && n >= 4 && n <= 4096);
+    d.B = 1;
+    EXPECT(gdn_linattn_workspace_size(&d, 1, &n) == GDN_ERR_INVALID_ARG);
+    EXPECT(gdn_linattn_chunk_fwd(&d, NULL, NULL, NULL, NULL, NULL, NULL, 0, 0, NULL, P(0), NULL, P(1), (size_t)1 << 60,
+                                 NULL) == GDN_ERR_INVALID_ARG);
+    d.T = 1;
+    d.H = 30000000000000LL;
+    EXPECT(gdn_linattn_workspace_size(&d, 0x7fffffff, &n) == GDN_ERR_INVALID_ARG);
+}
+
 int main(void) {
+    for (int32_t dt = 0; dt < 2; ++dt)
+        for (int32_t gate = 0; gate < 3; gate += 2) few_and_many_sequences(dt, gate);
+
     far_rows(1LL << 40);
     far_rows(1LL << 34);
     far_rows(1LL << 62);

@@ -4,6 +4,7 @@ GPU tests compare with are checked against independent forms."""
 import ctypes
 import os
 import re
+import time
 
 import numpy as np
 import pytest
@@ -106,6 +107,17 @@ def test_chunk_final_state_partly_over_initial(lib):
 def test_chunk_no_sequences_is_a_no_op(lib):
     assert _fwd(lib, _desc(B=0), ws=None) == gdn.GDN_OK
     assert _fwd(lib, _desc(B=1, T=0), cu=8, n=0, ws=None) == gdn.GDN_OK
+
+
+def test_chunk_no_sequences_takes_no_planning(lib):
+    """Without sequences there are no segments to weigh up, however many tokens each would have (2^26 chunks
+    here, each of which would count as a split to look at)."""
+    n = ctypes.c_size_t()
+    d = _desc(B=0, T=1 << 32)
+    start = time.perf_counter()
+    assert lib.gdn_linattn_workspace_size(ctypes.byref(d), 0, ctypes.byref(n)) == gdn.GDN_OK
+    assert _fwd(lib, d, ws=None) == gdn.GDN_OK
+    assert time.perf_counter() - start < 0.05
 
 
 def test_no_barrier_over_part_of_a_block():
