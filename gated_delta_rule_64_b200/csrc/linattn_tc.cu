@@ -766,20 +766,25 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 // at the segment's end
 // ===========================================================================
 // Backwards from the part's end: a token's weight is the sum of the gates after it, so the
-// products add up in TMEM without a rescale, and the kernel stops where nothing earlier
-// reaches the segment's end.  A segment is cut into parts so that the heads whose state
+// products add up without a rescale, and the kernel stops where nothing earlier reaches the
+// segment's end.  The products of kGroup chunks add up in TMEM; the tensor cores cut off what does
+// not fit an accumulator's 24 bits, always towards zero, so a long sum there comes out short
+// (2^-24 or so of it with every 16 tokens and term: 5e-5 of the state after 14,600 tokens that do not
+// fade).  The groups are added in registers, rounded to nearest: the warps of the terms
+// read one of two accumulators while the next group goes into the other.  A segment is cut into parts so that the heads whose state
 // lasts do not hold up the rest: their parts run side by side, and a part behind which the
 // decay has left nothing ends at once.
 // The weights of the whole part are formed first, 1024 tokens at a time by warps 0-15; then
 // these make the terms of V w (32 value channels and 16 tokens a warp, two buffers in TMEM),
-// warp 16 issues the MMAs and warp 17 the loads.  One block per SM (320 of 512 TMEM columns).
-// Measured: 121 us for 262,144 tokens of 16 heads with fixed decays (the heads whose state
-// lasts read all of k and v), 19 us for 4 x 4,096 tokens of 16 heads (bound by its start, the
+// warp 16 issues the MMAs and warp 17 the loads.  One block per SM (448 of 512 TMEM columns).
+// Measured: 129 us for 262,144 tokens of 16 heads with fixed decays (the heads whose state
+// lasts read all of k and v; 124 us with one accumulator for all chunks), 19 us for 4 x 4,096 tokens of 16 heads (bound by its start, the
 // gates and a few chunks).
 constexpr uint32_t kSsK = 0, kSsV = 16384, kSsStage = 32768;
 constexpr int kSsStages = 4;
 constexpr uint32_t kSsOffW = kSsStages * kSsStage;  // the part's weights, newest token last
-constexpr uint32_t kTmU = 0, kTmUT = 128;
+constexpr uint32_t kTmU = 0, kTmUT = 256;  // two accumulators, the terms
+constexpr int kGroup = 4;                  // chunks of an accumulator (two or more)
 constexpr int kTermWarps = 16, kTermThreads = kTermWarps * 32;
 constexpr int kStateThreads = (kTermWarps + 2) * 32;
 constexpr int kSpan = 2 * kTermThreads;  // tokens of a step of the scan
@@ -927,6 +932,25 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
         const int qd = warp & 3, tq = warp >> 2;  // channels 32 qd .., tokens 16 tq ..
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
         const uint32_t from = terms_address(smem_u32(sm + kSsV) + (uint32_t)(qd >> 1) * 8192u, (qd & 1) * 4, 16 * tq, lane);
+        float U[32];  // row 32 qd + lane, columns 32 tq ..
+#pragma unroll
+        for (int e = 0; e < 32; ++e) U[e] = 0.f;
+        int groups = 0;  // added
+        auto add_group = [&] {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float x[16];
+                tmem_ld16(tm + lane_off + kTmU + 128 * (groups & 1) + 32 * tq + 16 * q, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 y = __fadd2_rn(make_float2(U[16 * q + e], U[16 * q + e + 1]), make_float2(x[e], x[e + 1]));
+                    U[16 * q + e] = y.x;
+                    U[16 * q + e + 1] = y.y;
+                }
+            }
+            ++groups;
+        };
         for (int i = 0; i < nch; ++i) {
             const int stage = i % kSsStages;
             const float *w = wts + (most - 1 - i) * C + 16 * tq;
@@ -934,6 +958,8 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
             if (i >= 2) ok = ok && warp_wait(&bars.ds[i & 1], ((i >> 1) & 1) ^ 1);  // chunk i - 2 has used this buffer
             if (!ok) break;
             tc_fence_after();
+            // (its accumulator is written again a group later, after the terms that this warp makes below)
+            if (i >= 2 && (i - 1) % kGroup == 0) add_group();
 #pragma unroll
             for (int m = 0; m < 2; ++m) {  // 16 channels x 16 tokens each
                 uint32_t t0[4], t1[4], t2[4];
@@ -952,16 +978,10 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
             tc_fence_after();
         }
         if (ok) {
-            float *U = a.states + at * (int64_t)(D * D) + (int64_t)(qd * 32 + lane) * D + 32 * tq;
+            while (groups * kGroup < nch) add_group();  // (one or two)
+            float *to = a.states + at * (int64_t)(D * D) + (int64_t)(qd * 32 + lane) * D + 32 * tq;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float x[16];
-                tmem_ld16(tm + lane_off + kTmU + 32 * tq + 16 * q, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<float4 *>(U + 16 * q + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-            }
+            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(to + e) = make_float4(U[e], U[e + 1], U[e + 2], U[e + 3]);
             // the segment's decay (once it is past kDead, how far past does not matter)
             if (part == 0 && tid == 0) a.tot[s.ss * a.H + h] = fixed ? g64 * (double)s.len : (double)reach;
         }
@@ -974,7 +994,9 @@ gdn_linattn_state_tc(const __grid_constant__ CUtensorMap mk, const __grid_consta
             const uint64_t bk = sdesc_sw128(base + (i % kSsStages) * kSsStage + kSsK, 8192, 1024);
             const uint32_t t = tm + kTmUT + 96 * (i & 1);
 #pragma unroll
-            for (int m = 0; m < 3; ++m) mma4_ts<8, 128>(tm + kTmU, t + 32 * m, bk, idesc_bf16(128, 128, 0, 1), i > 0 || m > 0);
+            for (int m = 0; m < 3; ++m)
+                mma4_ts<8, 128>(tm + kTmU + 128 * (i / kGroup & 1), t + 32 * m, bk, idesc_bf16(128, 128, 0, 1),
+                                i % kGroup > 0 || m > 0);
             mma_commit_warp(&bars.ds[i & 1]);
             mma_commit_warp(&bars.empty[i % kSsStages]);
         }
