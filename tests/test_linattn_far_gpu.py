@@ -5,13 +5,17 @@ Tolerances: those of test_linattn_gpu.py (relative L2), except for states that v
 the tensor cores add 256 tokens in one accumulator, 48 products, each cut off by 2^-24 of it on average while it
 grows to its size (2/3 on average): 1.9e-6; the chunks of a segment that follow one another, 2,110, 2^-24
 sqrt(2110) = 2.7e-6; the products' own 1.3e-6 and the decays' 1.6e-6: together below 1e-5."""
+import numpy as np
 import pytest
 import torch
 
 from gated_delta_rule_64_b200 import gdn
+from oracle import linattn as L
+from tests.gpu_util import rel_l2
 
 pytestmark = pytest.mark.gpu
 
+TOL_F32 = 5e-6
 TOL_BF16 = 3 * 2.0 ** -8
 TOL_LONG = 1e-5
 
@@ -85,6 +89,96 @@ def test_chunk_states_of_a_long_memory():
     for i, h in enumerate(heads):
         assert _err(out[0, :, h], o[:, i]) <= TOL_BF16
         assert _err(fin[0, h], f[i]) <= TOL_LONG, (h, _err(fin[0, h], f[i]))
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("f32", 64, 64), ("bf16", 128, 64)])
+def test_chunk_cuda_cores_past_2_to_31_elements(dtype, dk, dv):
+    """1,040,000 tokens of 33 heads, 64 wide.  A token's decay is 0.25 or more, so what lies 1,000 tokens back
+    (2^-360) is gone."""
+    T, H, n = 1_040_000, 33, 2000
+    td = torch.float32 if dtype == "f32" else torch.bfloat16
+    gen = _gen(2)
+    q, k = (_unit(torch.randn(1, T, 1, dk, device="cuda", generator=gen)).to(td) for _ in range(2))
+    v = torch.randn(1, T, H, dv, device="cuda", generator=gen, dtype=td)
+    g = -0.25 - torch.rand(1, T, H, device="cuda", generator=gen)
+    out, fin, _ = gdn.gdn_linattn_chunk_fwd(q, k, v, g)
+    zero = torch.zeros(H, dv, dk, dtype=torch.float64, device="cuda")
+    o, f = _chunked(q[0, -n:].double().expand(n, H, dk), k[0, -n:].double().expand(n, H, dk), v[0, -n:].double(),
+                    g[0, -n:].double(), zero)
+    assert _err(fin[0], f) <= TOL_F32
+    assert _err(out[0, -1000:], o[-1000:]) <= (TOL_F32 if dtype == "f32" else 2.0 ** -8)
+    o, _ = _chunked(q[0, :n].double().expand(n, H, dk), k[0, :n].double().expand(n, H, dk), v[0, :n].double(),
+                    g[0, :n].double(), zero)
+    assert _err(out[0, :n], o) <= (TOL_F32 if dtype == "f32" else 2.0 ** -8)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+def test_chunk_snapshots_and_final_state_in_place_of_a_split(dtype, d):
+    """The start states are chained by a kernel of their own here, and the states at every 320 tokens are kept."""
+    rng = np.random.default_rng(3)
+    td = torch.float32 if dtype == "f32" else torch.bfloat16
+    t = lambda *s: torch.from_numpy(rng.standard_normal(s, dtype=np.float32))  # noqa: E731
+    q, k, v = _unit(t(2, 6000, 1, d)).to(td), _unit(t(2, 6000, 1, d)).to(td), t(2, 6000, 2, d).to(td)
+    g, h0 = -0.02 * t(2, 6000, 2).abs(), t(2, 2, d, d)
+    o, f, s = L.linear_attention(q, k, v, g, h0, snapshot_stride=320)
+    state = h0.cuda()
+    out, _, snaps = gdn.gdn_linattn_chunk_fwd(q.cuda(), k.cuda(), v.cuda(), g.cuda(), state, final_state=state,
+                                              snapshot_stride=320)
+    assert rel_l2(state, f) <= TOL_F32 and rel_l2(snaps, s) <= TOL_F32
+    assert rel_l2(out, o) <= (TOL_F32 if dtype == "f32" else TOL_BF16)
+
+
+def test_decode_states_past_2_to_31_elements():
+    B, H, d = 4100, 32, 128
+    gen = _gen(4)
+    r = lambda *s: torch.randn(s, device="cuda", generator=gen)  # noqa: E731
+    q, k, v, g = r(B, 1, H, d), r(B, 1, H, d), r(B, 1, H, d), -r(B, 1, H).abs()
+    state = r(B, H, d, d)
+    at = [0, B - 1]
+    s0 = state[at].double()
+    out = gdn.gdn_linattn_decode_step(q, k, v, g, state)
+    x = [y[at, 0].double() for y in (q, k, v, g)]
+    want = torch.exp(x[3])[..., None, None] * s0 + x[2][..., :, None] * x[1][..., None, :]
+    assert _err(state[at], want) <= TOL_F32
+    assert _err(out[at, 0], (want @ x[0][..., None])[..., 0]) <= TOL_F32
+
+
+def test_rope_past_2_to_31_elements_in_place():
+    T, hq, d = 66_000, 128, 256
+    gen = _gen(5)
+    q = torch.randn(1, T, hq, d, device="cuda", generator=gen, dtype=torch.bfloat16)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")[None]
+    f = (10000.0 ** (-torch.arange(128) / 128.0)).cuda()
+    at = [0, 1, T // 2, T - 1]
+    want = L.norm_rope(q[:, at], pos[:, at], f)
+    got, _ = gdn.gdn_qk_norm_rope(q, q[:, :, :0], pos, f, q_out=q)
+    assert got.data_ptr() == q.data_ptr() and rel_l2(got[:, at], want) <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rope_queries_only(dtype, interleaved, d):
+    """No key heads: an empty k, and nothing of it is touched."""
+    td = torch.float32 if dtype == "f32" else torch.bfloat16
+    for B, T, hq in ((1, 1, 1), (2, 33, 7), (300, 1, 16)):
+        gen = _gen(T)
+        q = torch.randn(B, T, hq, d, device="cuda", generator=gen).to(td)
+        pos = torch.randint(0, 5000, (B, T), device="cuda", generator=gen, dtype=torch.int32)
+        f = (10000.0 ** (-torch.arange(d // 4) / (d // 4))).float().cuda()
+        w = torch.randn(d, device="cuda", generator=gen)
+        y, none = gdn.gdn_qk_norm_rope(q, q[:, :, :0], pos, f, w, interleaved=interleaved)
+        assert none.shape == (B, T, 0, d)
+        want = L.norm_rope(q, pos, f, w, interleaved=interleaved)
+        assert rel_l2(y, want) <= (3e-6 if dtype == "f32" else 2.0 ** -8)
+
+
+def test_reorder_past_2_to_32_bytes():
+    """Twelve rows of 400 MB; one parent twice, one beam that nobody goes on with."""
+    state = torch.randint(0, 1 << 30, (12, 100_000_000), device="cuda", dtype=torch.int32, generator=_gen(6))
+    parent = torch.tensor([[1, 0, 3, 3], [0, 1, 2, 3], [3, 3, 0, 1]], dtype=torch.int32, device="cuda")
+    want = state[(parent.long() + 4 * torch.arange(3, device="cuda")[:, None]).flatten()]
+    assert torch.equal(gdn.gdn_state_reorder(state, parent), want)
 
 
 @pytest.fixture(autouse=True)
