@@ -155,6 +155,15 @@ __device__ __forceinline__ float2 exp2_pair(double x) {
     return make_float2(hi, (float)(e - (double)hi));
 }
 
+// The same for the sum x <= 0 of a chunk's gates in 32 bits: two floats where the state keeps most of itself
+// from chunk to chunk, and one where a rounding of 2^-24 a chunk, the same one every time if the
+// gates are alike, is forgotten after a dozen chunks.
+__device__ __forceinline__ float2 exp2_pair_f32(float x) {
+    if (!(x > -0.125f)) return make_float2(exp2f(x), 0.f);
+    const float m = expm1f(x * 0.693147180559945f), hi = 1.f + m;
+    return make_float2(hi, m - (hi - 1.f));  // (both differences are exact)
+}
+
 // The kernels of a call overlap at their ends: each lets the next one start (early), and the
 // next one waits for it before it touches what it wrote, in every block, so that the stream's
 // order holds for what follows the call.  The first kernel of a call is launched as usual.

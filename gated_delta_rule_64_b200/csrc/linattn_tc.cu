@@ -413,7 +413,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 float x[32];
                 tmem_ld32(tm + lane_off + kTmS + 64 * hf + 32 * q, x);
                 tmem_wait_ld();
-                if (d.y != 0.f)  // (a fixed decay, in two floats)
+                if (d.y != 0.f)  // (a fixed decay, or one close to 1: in two floats)
 #pragma unroll
                     for (int t = 0; t < 32; ++t) x[t] = fmaf(d.y, S[32 * q + t], x[t]);
 #pragma unroll
@@ -735,7 +735,7 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             if (lane == 0) {
                 fac.far = far;
                 fac.shift = __float2bfloat162_rn(ex2(-m));
-                fac.decay = !fixed ? make_float2(ex2(total), 0.f)
+                fac.decay = !fixed ? exp2_pair_f32(total)
                                    : (left >= C ? fixed_decay
                                                 : exp2_pair(gate2_exact(a.g[h]) * (double)left));
             }

@@ -91,6 +91,24 @@ def test_chunk_states_of_a_long_memory():
         assert _err(fin[0, h], f[i]) <= TOL_LONG, (h, _err(fin[0, h], f[i]))
 
 
+@pytest.mark.parametrize("gate", [-1.5e-5, -1.1e-4, -1.9e-3])
+def test_chunk_equal_gates_over_many_chunks(gate):
+    """Gates per token that are all alike, 2,110 chunks to a segment: every chunk's decay has the same rounding,
+    which must not be taken 2,110 times.  The decays' share of the tolerance, 1.6e-6, is that of one."""
+    B, T, H, d = 2, 270_000, 37, 128
+    gen = _gen(8)
+    q, k = (_unit(torch.randn(B, T, 1, d, device="cuda", generator=gen)).bfloat16() for _ in range(2))
+    v, h0 = (torch.randn(s, device="cuda", generator=gen, dtype=t) for s, t in
+             (((B, T, H, d), torch.bfloat16), ((B, H, d, d), torch.float32)))
+    g = torch.full((B, T, H), gate, device="cuda")
+    out, fin, _ = gdn.gdn_linattn_chunk_fwd(q, k, v, g, h0)
+    for b, h in ((0, 0), (1, H - 1)):
+        o, f = _chunked(*(x[b].double() for x in (q, k)), v[b, :, h:h + 1].double(), g[b, :, h:h + 1].double(),
+                        h0[b, h:h + 1].double())
+        assert _err(out[b, :, h], o[:, 0]) <= TOL_BF16
+        assert _err(fin[b, h], f[0]) <= TOL_LONG, _err(fin[b, h], f[0])
+
+
 @pytest.mark.parametrize("dtype,dk,dv", [("f32", 64, 64), ("bf16", 128, 64)])
 def test_chunk_cuda_cores_past_2_to_31_elements(dtype, dk, dv):
     """1,040,000 tokens of 33 heads, 64 wide.  A token's decay is 0.25 or more, so what lies 1,000 tokens back
