@@ -73,6 +73,25 @@ def test_chunk_segments_of_many_parts(gate, in_place):
             assert _err(fin[b, h], f[i]) <= TOL_LONG, (b, h, _err(fin[b, h], f[i]))
 
 
+@pytest.mark.parametrize("gate", ["token", "const"])
+def test_chunk_cuda_cores_equal_gates_over_a_long_segment(gate):
+    """270,000 fp32 tokens of 74 heads in two segments of 4,220 chunks; the state kept 64 tokens into the second
+    one is the first one's sum.  A sum of n = 135,040 products in a row, each rounded to 2^-23 / sqrt(12) of the
+    sum so far (rms), which grows like its root: 2^-23 sqrt(n / 24) = 8.9e-6, and 1.6e-6 for the decays: 1.1e-5.
+    The gate is one whose multiples round the same way in 32 bits, thousands of times."""
+    T, H, d, at = 270_000, 74, 64, 135_104
+    gen = _gen(9)
+    q, k = (_unit(torch.randn(1, T, 1, d, device="cuda", generator=gen)) for _ in range(2))
+    v = torch.randn(1, T, H, d, device="cuda", generator=gen)
+    x = -1.5274936e-05
+    g = torch.full((H,) if gate == "const" else (1, T, H), x, device="cuda")
+    _, _, snaps = gdn.gdn_linattn_chunk_fwd(q, k, v, g, snapshot_stride=at)
+    for h in (0, H - 1):
+        w = torch.exp(float(np.float32(x)) * torch.arange(at - 1, -1, -1, device="cuda", dtype=torch.float64))
+        want = (v[0, :at, h].double() * w[:, None]).T @ k[0, :at, 0].double()
+        assert _err(snaps[0, 0, h], want) <= 1.1e-5, _err(snaps[0, 0, h], want)
+
+
 def test_chunk_states_of_a_long_memory():
     """262,144 tokens that hardly fade (sums of -0.13): every segment's state is a sum over all that came before,
     none of which a biased rounding may shorten."""
