@@ -122,8 +122,12 @@ gdn_status gdn_qk_norm_rope(const gdn_qk_rope_desc *d, const void *q, const void
  * order is that of its logits).  A beam whose scores entry or whose sum is not finite (a
  * NaN or +infinite logit, no logit above -infinity, a finished beam marked with -infinity)
  * has all its scores at -infinity; continuations at -infinity come last, in index
- * order, and keep -infinity as their score.  The sums and scores are formed in 64
- * bits from fp32 exponentials, and rounded once.
+ * order, and keep -infinity as their score.  Exponentials, and their sums over up to
+ * 16,384 logits, are fp32; these sums are joined, and the scores formed and compared, in 64
+ * bits and rounded once.  A beam's log-sum is within 2^-17 (2^-22 is usual), the same for
+ * all its continuations: continuations of different beams whose scores are nearer than
+ * that may come in either order (beams with the same logits at the same places have the same
+ * log-sum).
  * ------------------------------------------------------------------------- */
 typedef struct gdn_beam_desc {
     int64_t B;          /* requests                                                     */

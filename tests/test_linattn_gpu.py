@@ -529,6 +529,30 @@ def test_beam_largest_vocabulary(dtype, V):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,V", [(1, 300), (1, 40_009), (40, 128_009)])
+def test_beam_log_sums(dtype, B, V):
+    """The stated bound of a beam's log-sum, at logits where many small exponentials add up.  For a logit d
+    below the slice's largest: its fp32 exponential is off by 2^-22 and by 2.25 d 2^-24 for the argument's two
+    roundings and the constant's, up to three times 2^-22 over the rescalings (whose d add up); 40 additions of
+    2^-24; d is log(16,384) = 9.7 on average at most.  Together (12 + 22 + 40) 2^-24 < 2^-17.  The score's own
+    rounding is 2^-24 of it."""
+    td = torch.float32 if dtype == "f32" else torch.bfloat16
+    x = torch.zeros(B, 4, V)
+    x[:, 1, 1:] = -9.6875
+    x[:, 2] = -torch.linspace(0, 20, V)
+    x[:, 3] = torch.randn(V, generator=torch.Generator().manual_seed(V)) * 4
+    x = x.to(td)
+    score, parent, token = (t.cpu() for t in gdn.gdn_beam_select(x.cuda(), None, 4))
+    lse = torch.logsumexp(x[0].double(), -1)
+    want = x[0].double() - lse[:, None]
+    for b in (0, B - 1):
+        at = want[parent[b].long(), token[b].long()]
+        assert ((score[b].double() - at).abs() <= 2.0 ** -17 + 2.0 ** -24 * at.abs()).all()
+    each = gdn.gdn_beam_select(x[:1].transpose(0, 1).contiguous().cuda(), None, 1)  # every beam on its own
+    assert ((each[0][:, 0].cpu().double() - (x[0].double().max(-1)[0] - lse)).abs() <= 2.0 ** -17 + 2.0 ** -20).all()
+
+
 def test_beam_first_step_and_strided_vocabulary():
     """All beams alike (the first step after a prompt): equal scores over beams, the first beam's come first;
     logits cut from rows of a padded vocabulary whose padding holds large values."""
