@@ -36,6 +36,14 @@ enum { GDN_GATE_CONST = 2 };
  * not finite makes the outputs of its 64-token chunk and of everything after it in
  * its sequence and head unspecified (other sequences and heads are not affected), and so
  * do sums of |q . k| |v| over a chunk of 2^67 or more (bf16, 128-wide heads).
+ *
+ * Precision.  States are fp32 sums of unrounded products: within 1e-5 (relative) over hundreds
+ * of thousands of tokens that do not fade, below 1e-6 as a rule.  Outputs are rounded once from fp32 sums, but for bf16 prompts with
+ * 128-wide heads (gdn_linattn_chunk_fwd, on the tensor cores): there the scores q . k, with
+ * their decays, and the state that meets q are rounded to bf16 first, once each, and where a
+ * chunk's decay is below 2^-120 the q that meets the state once more; outputs are then within
+ * 3 * 2^-8 (relative to their head's length; 2.3e-3 is usual, against 1.7e-3 for the last
+ * rounding alone), and contributions |q . k| |v| of less than 2^-64 may be lost.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace gdn_linattn_chunk_fwd needs for d->T tokens in num_seqs
@@ -86,8 +94,8 @@ gdn_status gdn_linattn_decode_step(const gdn_desc *d, const void *q, const void 
  *
  * for i < rot / 2, where (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) when
  * `interleaved`; channels from rot on are not rotated.  The norm and the rotation are in
- * fp32, the angle is formed and reduced in 64 bits (exact to fp32 at any int32
- * position, negative ones too), and the result is rounded once.
+ * fp32, the angle is formed and reduced in 64 bits (exact to fp32 up to a position times
+ * inv_freq of 2^27, negative ones too; within 2^-20 up to 2^31), and the result is rounded once.
  * ------------------------------------------------------------------------- */
 typedef struct gdn_qk_rope_desc {
     int64_t rows;       /* tokens (B * T)                                               */
