@@ -17,7 +17,7 @@
 // falls back on the K-th best of the threads' (value, index) pairs, of which at most K
 // threads have one, and the join on K rounds of a block-wide maximum.
 //
-// Measured: 32 requests of 8 beams, 128,009 bf16 logits, K = 16: 35 us.  The first kernel takes
+// Measured: 32 requests of 8 beams, 128,009 bf16 logits, K = 16: 34 us.  The first kernel takes
 // 25 us (the 66 MB alone are 10 us of HBM): each block's chain of load, maximum, bound and search,
 // and its instructions.  The second takes 14 us, a chain of dependent steps by 32 blocks, its
 // start hidden behind the first.
@@ -25,7 +25,7 @@
 // Reordering.  A thread owns 16 bytes of every beam's row of one request: it reads the
 // parents' bytes of all beams that change, then writes them, so the move is in place
 // without a second buffer and rows that stay are neither read nor written.  Measured: 256 states
-// of 2 MB, most of which change: 129 us, 0.80 GB at 6.2 TB/s (0.95 of a plain copy).
+// of 2 MB, most of which change: 127 to 134 us, 0.80 GB at 5.9 to 6.3 TB/s (0.91 to 0.96 of a plain copy).
 #include "linattn.cuh"
 #include "sm100.cuh"
 
@@ -455,7 +455,8 @@ gdn_state_reorder_kernel(uint4 *__restrict__ state, const int32_t *__restrict__ 
 int64_t slices_of(int64_t V, int each) { return (V + kThreads * each - 1) / (kThreads * each); }
 
 // Logits of a thread: 32, or 8 where slices of 8192 would leave SMs without one (4 beams of
-// 32,000: 23 us with 16 blocks, 19 with 64, of which the join takes 15 and 10), or 64 in bf16
+// 32,000: 23 us a call with 16 blocks, 19 with 64; 8.3 us of those are the kernels' in a captured
+// graph), or 64 in bf16
 // where that still gives every SM four blocks (256 beams of 128,009: 35 us a call against 39, of
 // which the join, with half the candidates, gives two).
 int each(const gdn_beam_desc &d) {

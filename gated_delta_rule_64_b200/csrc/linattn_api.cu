@@ -73,7 +73,10 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
     p.dv = d.dv;
     p.packed = packed;
     p.fixed_gate = d.gate == GDN_GATE_CONST;
-    // bf16 with 128-wide heads on the tensor cores, all else on the CUDA cores
+    // bf16 with 128-wide heads on the tensor cores, whose kernels are laid out for that width, all
+    // else on the CUDA cores.  4 sequences of 4,096 tokens and 16 heads: 78 us there; here 490 us
+    // with 64-wide bf16 heads, 770 (keys) and 890 (values) with one side 128 wide, 520 and 1,410
+    // with 64- and 128-wide fp32 heads (of which each operand would take three bf16 terms).
     p.tc = d.dtype == GDN_BF16 && d.dk == 128 && d.dv == 128;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -97,8 +100,8 @@ Plan make_plan(const gdn_desc &d, int64_t num_seqs, bool packed) {
     // Parts of a segment's state (tensor cores), of four chunks or more and kMaxPart tokens or
     // fewer.  With a fixed gate a block sees at once whether its part reaches the segment's
     // end, and heads whose state lasts work side by side: four parts (262,144 tokens of 16
-    // heads, state and output kernel: 181 + 759 us with one part, 121 + 779 with four, 114 +
-    // 808 with eight, which the output kernel's blocks have to add up).  With a gate per token
+    // heads, state and output kernel: 186 + 796 us with one part, 126 + 802 with four, 118 +
+    // 822 with eight, which the output kernel's blocks have to add up).  With a gate per token
     // it has to add up the gates behind its part first, 3 us even where it then has nothing to
     // do, at one block per SM: about two blocks per SM in all (4 x 4,096 tokens of 16 heads: 32
     // us with eight parts, 19 with two).  The CUDA-core state kernel takes a segment whole (it

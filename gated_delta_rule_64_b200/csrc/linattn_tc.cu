@@ -44,8 +44,10 @@
 // A chunk moves 64 KB (q, k, v, out): 1.5 us of an SM's share of the HBM bandwidth.  Its MMAs
 // take about 1500 cycles (measured alone: 37 cycles for 128 x 64 x 16 with A in TMEM, 54 with
 // A in shared memory, 69 for 128 x 128 x 16).  Measured: one sequence of 262,144 tokens and 16
-// heads, 780 us (1.76 us a chunk and SM, 5.5 TB/s: HBM, and the warps of V w close behind it); 4
-// sequences of 4,096 tokens, 62 us (128 blocks of 32 chunks at 1.8 us, and the start).
+// heads, 800 us at 1,965 MHz (1.8 us a chunk and SM, 5.4 TB/s); a call in a steady loop, which the
+// power cap holds at 1,410 MHz, takes 1,100 us instead of 930, so a chunk's chain of products and
+// the warps' work between them set the pace, not HBM.  4 sequences of 4,096 tokens, 64 us (128
+// blocks of 32 chunks, and the start).
 #include <cudaTypedefs.h>
 #include <string.h>
 
