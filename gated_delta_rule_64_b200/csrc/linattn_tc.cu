@@ -773,15 +773,15 @@ gdn_linattn_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 // not fit an accumulator's 24 bits, always towards zero, so a long sum there comes out short
 // (2^-24 or so of it with every 16 tokens and term: 5e-5 of the state after 14,600 tokens that do not
 // fade).  The groups are added in registers, rounded to nearest: the warps of the terms
-// read one of two accumulators while the next group goes into the other.  A segment is cut into parts so that the heads whose state
-// lasts do not hold up the rest: their parts run side by side, and a part behind which the
-// decay has left nothing ends at once.
+// read one of two accumulators while the next group goes into the other.
+// A segment is cut into parts so that the heads whose state lasts do not hold up the rest: their
+// parts run side by side, and a part behind which the decay has left nothing ends at once.
 // The weights of the whole part are formed first, 1024 tokens at a time by warps 0-15; then
 // these make the terms of V w (32 value channels and 16 tokens a warp, two buffers in TMEM),
 // warp 16 issues the MMAs and warp 17 the loads.  One block per SM (448 of 512 TMEM columns).
 // Measured: 129 us for 262,144 tokens of 16 heads with fixed decays (the heads whose state
-// lasts read all of k and v; 124 us with one accumulator for all chunks), 19 us for 4 x 4,096 tokens of 16 heads (bound by its start, the
-// gates and a few chunks).
+// lasts read all of k and v; 124 us with one accumulator for all chunks), 19 us for 4 x 4,096
+// tokens of 16 heads (bound by its start, the gates and a few chunks).
 constexpr uint32_t kSsK = 0, kSsV = 16384, kSsStage = 32768;
 constexpr int kSsStages = 4;
 constexpr uint32_t kSsOffW = kSsStages * kSsStage;  // the part's weights, newest token last

@@ -38,12 +38,13 @@ enum { GDN_GATE_CONST = 2 };
  * do sums of |q . k| |v| over a chunk of 2^67 or more (bf16, 128-wide heads).
  *
  * Precision.  States are fp32 sums of unrounded products: within 1e-5 (relative) over hundreds
- * of thousands of tokens that do not fade, below 1e-6 as a rule.  Outputs are rounded once from fp32 sums, but for bf16 prompts with
- * 128-wide heads (gdn_linattn_chunk_fwd, on the tensor cores): there the scores q . k, with
- * their decays, and the state that meets q are rounded to bf16 first, once each, and where a
- * chunk's decay is below 2^-120 the q that meets the state once more; outputs are then within
- * 3 * 2^-8 (relative to their head's length; 2.3e-3 is usual, against 1.7e-3 for the last
- * rounding alone), and contributions |q . k| |v| of less than 2^-64 may be lost.
+ * of thousands of tokens that do not fade, below 1e-6 as a rule.  Outputs are rounded once from
+ * fp32 sums, but for bf16 prompts with 128-wide heads (gdn_linattn_chunk_fwd, on the tensor
+ * cores): there the scores q . k, with their decays, and the state that meets q are rounded to
+ * bf16 first, once each, and where a chunk's decay is below 2^-120 the q that meets the state
+ * once more; outputs are then within 3 * 2^-8 (relative to their head's length; 2.3e-3 is
+ * usual, against 1.7e-3 for the last rounding alone), and contributions |q . k| |v| of less
+ * than 2^-64 may be lost.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace gdn_linattn_chunk_fwd needs for d->T tokens in num_seqs
