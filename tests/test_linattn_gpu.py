@@ -137,6 +137,18 @@ def test_chunk_large_values_under_strong_decays(dtype, log2_decay):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("log2_decay", [-40.0, -100.0, -119.0, -121.0])
+def test_chunk_small_values_under_strong_decays(dtype, log2_decay):
+    """The other end: contributions |q . k| |v| near 2^-53.  On the tensor cores a factor of 2^-60 meets them, and
+    2^-126 is the least normal value, so that what is lost there (below 2^-64) is rarer than one in 2^10
+    of them, each 2^-11 of the others."""
+    x = _inputs(1, 200, 2, 1, 128, 128, dtype, seed=23)
+    x["v"], x["h0"] = x["v"] * 2.0 ** -50, x["h0"] * 2.0 ** -50
+    x["g"][:] = log2_decay * float(np.log(2.0)) / 64
+    _check(x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("erase", [torch.finfo(torch.float32).min, float("-inf"), -106.0])
 @pytest.mark.parametrize("T", [200, 3000])
 def test_chunk_gates_of_the_lowest_value(dtype, erase, T):
